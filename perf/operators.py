@@ -150,6 +150,8 @@ def prepare(case, seed):
     s["a"] = _encode(normal(N, k))
     s["w"] = _encode(normal(E * n, k, std=1.0 / math.sqrt(k)))
     s["w3"] = _encode(normal(E * n, k, std=1.0 / math.sqrt(k))) if c["swiglu"] else None
+    # a program lays its weights' scales out once, as the product reads them
+    s["tiles"] = [_tiled(v[1]) for v in (s["w"], s["w3"]) if v is not None]
     return s
 
 
@@ -270,6 +272,12 @@ def _encode(x):
     return code[:, :, 0] | (code[:, :, 1] << 4), (e + 127).to(torch.uint8).reshape(x.shape[0], -1)
 
 
+def _tiled(scales):
+    """The scales in tiles of 128 rows by 4 blocks, as the product reads its weights'."""
+    t = scales.reshape(scales.shape[0] // 128, 4, 32, scales.shape[1] // 4, 4)
+    return t.permute(0, 3, 2, 1, 4).contiguous().reshape(scales.shape)
+
+
 def _decode(codes, scales):
     grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0], device=codes.device)
     v = torch.stack([grid[(codes & 15).int()], grid[(codes >> 4).int()]], dim=2).reshape(codes.shape[0], -1, 32)
@@ -342,8 +350,8 @@ def _own(s):
     if not keep:
         keep["dsc"] = abi.mx4_desc(c["N"], c["E"], c["n"], c["k"], swiglu=c["swiglu"], out=c["out"])
         keep["ws"] = abi.alloc_mx4_workspace(keep["dsc"])
-    w3, s3 = s["w3"] if c["swiglu"] else (None, None)
-    abi.mx4_expert_product(keep["dsc"], s["a"][0], s["a"][1], s["counts"], s["w"][0], s["w"][1], s["out"], keep["ws"], w3_codes=w3, w3_scales=s3)
+    w3, t3 = (s["w3"][0], s["tiles"][1]) if c["swiglu"] else (None, None)
+    abi.mx4_expert_product(keep["dsc"], s["a"][0], s["a"][1], s["counts"], s["w"][0], s["tiles"][0], s["out"], keep["ws"], w3_codes=w3, w3_scales=t3)
     return s["out"]
 
 

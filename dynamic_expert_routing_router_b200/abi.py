@@ -35,6 +35,11 @@ class Desc(ctypes.Structure):
                 ("n_shared", ctypes.c_int), ("I_shared", ctypes.c_int)]
 
 
+class Mx4Desc(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("E", ctypes.c_int), ("n", ctypes.c_int),
+                ("k", ctypes.c_int), ("swiglu", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("BN", ctypes.c_int), ("router_bn", ctypes.c_int),
                 ("router_splits", ctypes.c_int), ("p_cap", ctypes.c_int),
@@ -98,6 +103,17 @@ def lib():
         L.beam_moe_tau_to_logit.restype = ctypes.c_float
         L.beam_moe_set_fault_injection.argtypes = [i32, ctypes.c_ulonglong]
         L.beam_moe_set_fault_injection.restype = i32
+        i64 = ctypes.c_longlong
+        L.beam_mx4_quantize.argtypes = [i32, i64, i32, vp, vp, vp, vp, i32, vp]
+        L.beam_mx4_dequantize.argtypes = [i32, i64, i32, vp, vp, i32, vp, vp]
+        pm = ctypes.POINTER(Mx4Desc)
+        L.beam_mx4_workspace_size.argtypes = [pm]
+        L.beam_mx4_workspace_size.restype = sz
+        L.beam_mx4_expert_product.argtypes = [pm, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_mx4_check.argtypes = [pm, vp, vp]
+        for f in ("beam_mx4_quantize", "beam_mx4_dequantize", "beam_mx4_expert_product",
+                  "beam_mx4_check"):
+            getattr(L, f).restype = i32
         L.beam_status_str.argtypes = [i32]
         L.beam_status_str.restype = ctypes.c_char_p
         L.beam_moe_stage_name.argtypes = [i32]
@@ -239,6 +255,7 @@ def route_noalloc_check(stream=None):
 
 
 FAULT_NONE, FAULT_EXPERT_STAGE, FAULT_ROUTER_STAGE, FAULT_SHARED_STAGE = 0, 1, 2, 3
+FAULT_MX4_STAGE = 4
 
 
 def set_fault_injection(mode: int, wait_limit_ns: int = 0):
@@ -297,6 +314,124 @@ def ep_combine(dsc, y_rows, topk_idx, topk_w, pair_pos, out, stream=None):
     _ok(lib().beam_moe_ep_combine(ctypes.byref(dsc), _ptr(y_rows), _ptr(topk_idx),
                                   _ptr(topk_w), _ptr(pair_pos), _ptr(out), _stream(stream)),
         "beam_moe_ep_combine")
+
+
+# ------------------------------------------------------ checked arguments --
+# The calls below take whole tensors, not buffers with a descriptor's word for
+# their size, so the binding refuses what the library cannot see: another
+# dtype or shape, strides, another device than the current one.
+
+def _code(dtype):
+    return dtype if isinstance(dtype, int) else (BEAM_BF16 if dtype == "bf16" else BEAM_F32)
+
+
+def _torch_dtype(code):
+    import torch
+    return torch.bfloat16 if code == BEAM_BF16 else torch.float32
+
+
+def _arg(what, name, t, dtype, shape, optional=False):
+    """The address of tensor `t`, which has to be a contiguous `dtype` tensor
+    of `shape` on the current device; None where it may be left out."""
+    if t is None:
+        if optional:
+            return None
+        raise BeamError(1, f"{what}: {name} is missing")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise BeamError(1, f"{what}: {name} has to be a contiguous {dtype} tensor of shape "
+                           f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device.type != "cuda" or t.device.index != _current_device():
+        raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
+    return t.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+# ------------------------------------------- experts in 4-bit floating point --
+
+def _mx4_rows(what, x, codes, scales):
+    import torch
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise BeamError(1, f"{what}: a bf16 or f32 matrix is wanted, got {x.dtype} "
+                           f"{tuple(x.shape)}")
+    rows, cols = x.shape
+    if cols % 32:
+        raise BeamError(2, f"{what}: {cols} columns are no multiple of 32")
+    code = BEAM_BF16 if x.dtype == torch.bfloat16 else BEAM_F32
+    return (code, rows, cols, _arg(what, "values", x, x.dtype, (rows, cols)),
+            _arg(what, "codes", codes, torch.uint8, (rows, cols // 2)),
+            _arg(what, "scales", scales, torch.uint8, (rows, cols // 32)))
+
+
+def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
+    """x [rows, cols] (bf16 or f32) to MXFP4: codes uint8 [rows, cols / 2],
+    scales uint8 [rows, cols / 32]; tiled: the scales in the tiles the product
+    reads its weights' from.  n_rows: int32 [1] on the device, the rows that
+    are there (the others are left as they are)."""
+    import torch
+    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_quantize", x, codes, scales)
+    pn = _arg("beam_mx4_quantize", "n_rows", n_rows, torch.int32, (1,), optional=True)
+    _ok(lib().beam_mx4_quantize(code, rows, cols, px, pn, pc, ps, int(tiled), _stream(stream)),
+        "beam_mx4_quantize")
+
+
+def mx4_dequantize(codes, scales, out, tiled=False, stream=None):
+    """The values of an MXFP4 matrix, out [rows, cols] bf16 or f32."""
+    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_dequantize", out, codes, scales)
+    _ok(lib().beam_mx4_dequantize(code, rows, cols, pc, ps, int(tiled), px, _stream(stream)),
+        "beam_mx4_dequantize")
+
+
+def mx4_desc(N, E, n, k, swiglu=False, out="bf16") -> Mx4Desc:
+    """One grouped projection: capacity of N token rows of width k, E experts
+    of n weight rows; swiglu: gate and up; out: the output's dtype."""
+    return Mx4Desc(int(N), int(E), int(n), int(k), int(swiglu), _code(out))
+
+
+def mx4_workspace_size(dsc: Mx4Desc) -> int:
+    return int(lib().beam_mx4_workspace_size(ctypes.byref(dsc)))
+
+
+def alloc_mx4_workspace(dsc: Mx4Desc, device=None):
+    """A uint8 torch tensor of mx4_workspace_size(dsc) bytes on `device`."""
+    import torch
+    n = mx4_workspace_size(dsc)
+    if n == 0:
+        raise BeamError(1, "beam_mx4_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, workspace,
+                       w3_codes=None, w3_scales=None, stream=None):
+    """out[i] = a_i w_e^T for the rows i of expert e (grouped by expert, counts
+    int32 [E] on the device), or SiLU(a_i w_e^T) * (a_i w3_e^T) when
+    dsc.swiglu.  w_scales, w3_scales: tiled (mx4_quantize(..., tiled=True))."""
+    import torch
+    what, u8 = "beam_mx4_expert_product", torch.uint8
+    N, E, n, k = dsc.N, dsc.E, dsc.n, dsc.k
+    wc, ws = (E * n, k // 2), (E * n, k // 32)
+    if dsc.swiglu == 0 and (w3_codes is not None or w3_scales is not None):
+        raise BeamError(1, f"{what}: a second weight without swiglu")
+    second = dsc.swiglu != 0
+    _ok(lib().beam_mx4_expert_product(
+        ctypes.byref(dsc), _arg(what, "a_codes", a_codes, u8, (N, k // 2)),
+        _arg(what, "a_scales", a_scales, u8, (N, k // 32)),
+        _arg(what, "counts", counts, torch.int32, (E,)),
+        _arg(what, "w_codes", w_codes, u8, wc), _arg(what, "w_scales", w_scales, u8, ws),
+        _arg(what, "w3_codes", w3_codes, u8, wc) if second else None,
+        _arg(what, "w3_scales", w3_scales, u8, ws) if second else None,
+        _arg(what, "out", out, _torch_dtype(dsc.out_dtype), (N, n)),
+        _arg(what, "workspace", workspace, u8, workspace.shape), workspace.numel(),
+        _stream(stream)), what)
+
+
+def mx4_check(dsc, workspace, stream=None):
+    """Synchronise and read the status of the last product on `workspace`."""
+    _ok(lib().beam_mx4_check(ctypes.byref(dsc), _ptr(workspace), _stream(stream)),
+        "beam_mx4_check")
 
 
 def check(dsc, workspace, stream=None):

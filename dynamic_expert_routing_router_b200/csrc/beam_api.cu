@@ -257,6 +257,8 @@ TmapCache &tmap_cache() {
 // chunks > 0: a 3D view [inner / 64][rows][64] of the same matrix whose box
 // is `chunks` consecutive 64-column chunks of box_rows rows: one copy lands
 // them as `chunks` swizzled 64-column boxes, one after another.
+// chunks = kByteMap: `inner` bytes per row and a box of 128 bytes x box_rows.
+constexpr unsigned kByteMap = ~0u;
 bool make_tmap(CUtensorMap *m, const void *base, unsigned long long inner,
                unsigned long long rows, unsigned box_rows, unsigned chunks = 0) {
     const TmapKey key{base, inner, rows, box_rows, chunks};
@@ -273,7 +275,15 @@ bool make_tmap(CUtensorMap *m, const void *base, unsigned long long inner,
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn || rows == 0) return false;
     CUresult r;
-    if (chunks == 0) {
+    if (chunks == kByteMap) {
+        cuuint64_t dims[2] = {inner, rows};
+        cuuint64_t strides[1] = {inner};
+        cuuint32_t box[2] = {128, box_rows};
+        cuuint32_t estr[2] = {1, 1};
+        r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else if (chunks == 0) {
         cuuint64_t dims[2] = {inner, rows};
         cuuint64_t strides[1] = {inner * 2};
         cuuint32_t box[2] = {unsigned(kBlockK), box_rows};
@@ -1059,6 +1069,14 @@ beam_status backward_impl(const beam_moe_desc *d, const void *x, const void *Wg,
 
 namespace beam {
 
+int device_sm_count() { return sm_count(); }
+unsigned long long device_wait_limit_ns() { return wait_limit_ns(); }
+int device_fault_mode() { return fault_mode(); }
+bool make_byte_tmap(CUtensorMap *m, const void *base, unsigned long long row_bytes,
+                    unsigned long long rows, unsigned box_rows) {
+    return make_tmap(m, base, row_bytes, rows, box_rows, kByteMap);
+}
+
 size_t route_scratch_bytes(const beam_moe_desc *desc) {
     beam_moe_plan_info P;
     if (make_plan(desc, &P) != BEAM_OK) return 0;
@@ -1326,7 +1344,7 @@ float beam_moe_tau_to_logit(float tau) {
 
 beam_status beam_moe_set_fault_injection(int mode, unsigned long long wait_limit_ns) {
     if (mode != FAULT_NONE && mode != FAULT_EXPERT_STAGE && mode != FAULT_ROUTER_STAGE &&
-        mode != FAULT_SHARED_STAGE)
+        mode != FAULT_SHARED_STAGE && mode != FAULT_MX4_STAGE)
         return BEAM_ERR_INVALID_ARG;
     g_fault.store(mode, std::memory_order_relaxed);
     g_wait_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);

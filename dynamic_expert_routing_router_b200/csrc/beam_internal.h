@@ -31,7 +31,22 @@ constexpr int kHdrErr = 0, kHdrErrRouter = 1, kHdrErrShared = 2, kHdrMeta = 4;  
 
 // Fault injection for tests (beam_moe_set_fault_injection): which launch skips
 // one stage load in CTA 0 so that its MMA issuer's bounded wait expires.
-enum : int { FAULT_NONE = 0, FAULT_EXPERT_STAGE = 1, FAULT_ROUTER_STAGE = 2, FAULT_SHARED_STAGE = 3 };
+enum : int {
+    FAULT_NONE = 0,
+    FAULT_EXPERT_STAGE = 1,
+    FAULT_ROUTER_STAGE = 2,
+    FAULT_SHARED_STAGE = 3,
+    FAULT_MX4_STAGE = 4
+};
+
+// Host state shared by the entry points (beam_api.cu).
+int device_sm_count();                      // of the current device
+unsigned long long device_wait_limit_ns();  // of every bounded device wait
+int device_fault_mode();                    // FAULT_*
+// 2D map over row-major bytes [rows, row_bytes], box 128 bytes x box_rows,
+// 128-byte swizzle, zero fill.
+bool make_byte_tmap(CUtensorMap *m, const void *base, unsigned long long row_bytes,
+                    unsigned long long rows, unsigned box_rows);
 
 // Roles of the tensor-core GEMM kernel.
 enum TcMode : int {
@@ -340,6 +355,21 @@ cudaError_t launch_backward_stages(const BwArgs &a, int dtype, const void *x, co
                                    const void *Wm, const void *W1, const void *W3,
                                    const void *W2, float *dWg, float *dWm, float *dW1,
                                    float *dW3, float *dW2, int n_sm, cudaStream_t st, int phase);
+
+// Grouped expert product of 4-bit operands (mx4.cu).
+struct Mx4Maps {
+    CUtensorMap w, w3, a;  // codes of the weights [E n, k / 2] and the token rows [N, k / 2]
+};
+struct Mx4Args {
+    int N, E, n, k, out_f32;
+    const int *counts;          // [E] token rows per expert
+    const uint8_t *a_scales;    // [N][k / 32]
+    const uint8_t *w_scales, *w3_scales;  // tiled, see tiled_at
+    void *out;                  // [N][n]
+    int *status;                // workspace: [0] CTAs, [64 + b] CTA b's DEV_* status
+    unsigned long long timeout_ns;
+    int fault_skip;             // tests: CTA 0 skips its first stage
+};
 
 // fp32 SIMT path (BEAM_F32).
 cudaError_t launch_router_f32(const float *x, const float *Wg, const float *Wm, int T, int d,

@@ -1,0 +1,791 @@
+// mx4.cu -- microscaled 4-bit floating point (MXFP4): rows to 4 bits and back,
+// and the grouped expert product of two such matrices.
+//
+// The format (OCP Microscaling v1.0): 32 consecutive values of a row share one
+// power of two 2^X, X = floor(log2 max|v|) - 2, kept as the byte X + 127; each
+// value is v / 2^X rounded to nearest-even on the grid +-{0, .5, 1, 1.5, 2, 3,
+// 4, 6} (E2M1), larger magnitudes saturating at 6.
+#include <cuda_bf16.h>
+
+#include "beam_internal.h"
+#include "beam_ptx.cuh"
+
+namespace beam {
+namespace {
+
+// ------------------------------------------------------------- quantise --
+// Four lanes share a block of 32 values, eight each: a warp reads 512
+// contiguous bytes of bf16 per load and writes 128 of codes.  Scaling by 2^-X
+// is exact, so each value is rounded once, by the conversion.
+
+__device__ __forceinline__ void load_eight(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 r = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load_eight(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// Two values to E2M1 (round to nearest even, saturating): lo in bits 0-3.
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+        "cvt.u32.u8 %0, b;\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Byte of the scale of (row, block) in the tiled layout the product reads:
+// tiles of 128 rows x 4 blocks of 512 bytes, row r of a tile at 16 (r % 32) +
+// 4 (r / 32), its four blocks side by side.
+__device__ __forceinline__ long long tiled_at(long long row, int block, int blocks) {
+    const int r = int(row & 127);
+    return ((row >> 7) * (blocks >> 2) + (block >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 +
+           (block & 3);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, long long rows, int cols,
+                                                           const int *n_rows, uint32_t *codes,
+                                                           uint8_t *scales, int tiled) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (n_rows) {
+        const long long n = *n_rows;
+        rows = n < 0 ? 0 : n < rows ? n : rows;
+    }
+    const long long total = rows * (cols >> 3);  // eights; a block's four never split
+    const int blocks = cols >> 5;
+    const long long step = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        float v[8];
+        load_eight(x + i * 8, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        const unsigned quad = 0xfu << (threadIdx.x & 28);
+        m = max(m, __shfl_xor_sync(quad, m, 1));
+        m = max(m, __shfl_xor_sync(quad, m, 2));
+        const int field = int(m >> 23);  // exponent + 127 of the largest; 0: subnormal or zero
+        const bool bad = field == 255;   // infinity or NaN: the whole block stands for NaN
+        const int s = field > 2 ? field - 2 : 0;
+        const float inv = __uint_as_float(uint32_t(254 - s) << 23);  // 2^-X
+        uint32_t out = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            out |= to_e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+        codes[i] = bad ? 0u : out;
+        if ((threadIdx.x & 3) == 0) {
+            const long long b = i >> 2;
+            long long at = b;
+            if (tiled) at = tiled_at(b / blocks, int(b % blocks), blocks);
+            scales[at] = bad ? 255 : uint8_t(s);
+        }
+    }
+}
+
+// ----------------------------------------------------------- read back --
+
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    // 3-bit magnitude as bits of a float with exponent field 126 + ..: the
+    // subnormal code 1 is 0.5, codes 2..7 are (1 + m/2) 2^(e-1).
+    const uint32_t a = c & 7u;
+    const float v = a < 2u ? 0.5f * float(a)
+                           : __uint_as_float(((a >> 1) + 126u) << 23 | (a & 1u) << 22);
+    return (c & 8u) ? -v : v;
+}
+
+__device__ __forceinline__ void store_eight(__nv_bfloat16 *p, const float (&v)[8]) {
+    __nv_bfloat162 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+}
+__device__ __forceinline__ void store_eight(float *p, const float (&v)[8]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *codes,
+                                                             const uint8_t *scales,
+                                                             long long rows, int cols, int tiled,
+                                                             T *out) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long total = rows * (cols >> 3);
+    const int blocks = cols >> 5;
+    const long long step = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        const uint32_t c = codes[i];
+        const long long b = i >> 2;
+        const uint32_t s = scales[tiled ? tiled_at(b / blocks, int(b % blocks), blocks) : b];
+        // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
+        const float f = s == 0 ? __uint_as_float(0x00400000u)
+                               : __uint_as_float(s == 255u ? 0x7fc00000u : s << 23);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * f;
+        store_eight(out + i * 8, v);
+    }
+}
+
+// -------------------------------------------------------------- product --
+// out[i, :] = a_i . w_e^T for the rows i of expert e (rows grouped by expert,
+// counts on the device), or SiLU(a_i . w_e^T) * (a_i . w3_e^T).
+//
+// tcgen05.mma kind::mxf4 takes both 4-bit operands and their scales as they
+// are.  The weight rows are the MMA's M (128 per tile), the token rows its N
+// (16..BN, following the tile's valid rows), so a decode batch, bound by the
+// weights' bytes, wastes no tile on tokens it lacks.
+//
+// One persistent CTA per SM; unit = (token tile, 128 weight rows).  Warps:
+//   0     TMA of both code tiles (128 bytes = 256 values a row and stage) and
+//         bulk copies of the weight scales, which lie in memory as tiled_at
+//   1     TMEM owner and issuer: copies a stage's scales to TMEM
+//         (tcgen05.cp, in order with the MMAs of the same thread), 4 MMAs
+//   2..5  epilogue
+//   6     the token rows' scales: they start at any row, so this warp loads
+//         them row by row, a step ahead, and lays them out in the stage
+// Every wait is bounded; on expiry the CTA's status word says so.
+
+constexpr int kMxThreads = 224;
+constexpr int kMxStepK = 256;             // values per stage: one 128-byte row
+constexpr uint32_t kMxSfCols = 64;        // TMEM columns of scales, behind the accumulators
+constexpr uint32_t kMxTmemCols = 512;
+constexpr uint32_t kMxSfChunk = 512;      // bytes of one 128 x 4 tile of scales
+
+template <int NUM_A, int BN>
+struct MxCfg {
+    static constexpr uint32_t A_BYTES = 128 * 128;
+    static constexpr uint32_t B_BYTES = BN * 128;
+    static constexpr uint32_t B_SF_TILES = (BN + 127) / 128;  // per 4 blocks of k
+    static constexpr uint32_t SFA_BYTES = 2 * kMxSfChunk;
+    static constexpr uint32_t SFB_BYTES = 2 * kMxSfChunk * B_SF_TILES;
+    static constexpr uint32_t OFF_B = NUM_A * A_BYTES;
+    static constexpr uint32_t OFF_SFA = OFF_B + B_BYTES;
+    static constexpr uint32_t OFF_SFB = OFF_SFA + NUM_A * SFA_BYTES;
+    static constexpr uint32_t STAGE_BYTES = (OFF_SFB + SFB_BYTES + 1023) / 1024 * 1024;
+    static constexpr int STAGES_FIT = int(220u * 1024u / STAGE_BYTES);
+    static constexpr int STAGES = STAGES_FIT > 10 ? 10 : STAGES_FIT;
+    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+    static constexpr uint32_t ACC_COLS = NUM_A * BN;
+    static constexpr uint32_t ACC_BUFS = 2 * ACC_COLS <= kMxTmemCols - kMxSfCols ? 2 : 1;
+    // scales of one stage in TMEM, two stages in turn
+    static constexpr uint32_t SF_COLS = 2 * 4 * (NUM_A + B_SF_TILES);
+    static_assert(ACC_BUFS * ACC_COLS <= kMxTmemCols - kMxSfCols, "accumulators and scales share TMEM");
+    static_assert(2 * SF_COLS <= kMxSfCols, "scales in TMEM");
+    static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
+    static_assert(B_BYTES % 1024 == 0, "1024-byte aligned tiles");
+    static_assert(STAGES >= 2 && SMEM_BYTES <= 227u * 1024u - 4096u, "shared memory");
+};
+
+// Instruction descriptor of kind::mxf4: A and B E2M1 (1) at [7,10) and
+// [10,12), N >> 3 at [17,23), scales UE8M0 (1) at 23, M >> 7 at [27,29), the
+// scale bytes' ids of B at [4,6) and of A at [29,31); both operands K-major,
+// K = 64.
+__device__ __forceinline__ uint32_t mxf4_idesc(int n, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (1u << 23) |
+           (1u << 27) | (sf_id << 29);
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// One 512-byte tile of scales (32 rows of 16 bytes, no swizzle: 8-row groups
+// of 128 bytes) to four TMEM columns, the same in all four lane quadrants.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
+    uint64_t desc = 0;
+    desc |= uint64_t((smem_addr & 0x3FFFFu) >> 4);
+    desc |= uint64_t(128u >> 4) << 32;
+    desc |= uint64_t(1u) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(smem_dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+struct MxUnit {
+    int e, mb;      // expert, block of 128 weight rows
+    int row, rows;  // first token row, valid rows
+};
+
+// tile_end[e]: tiles of the experts up to e; row_end[e]: their rows.
+__device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int bn, int E, const int *tile_end,
+                                          const int *row_end) {
+    MxUnit w;
+    const int t = u / n_mb;
+    w.mb = u - t * n_mb;
+    int lo = 0, hi = E - 1;  // the first expert with tile_end > t
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tile_end[mid] > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    w.e = lo;
+    const int t0 = lo ? tile_end[lo - 1] : 0, r0 = lo ? row_end[lo - 1] : 0;
+    w.row = r0 + (t - t0) * bn;
+    w.rows = min(bn, row_end[lo] - w.row);
+    return w;
+}
+
+__device__ __forceinline__ int mx_cols(int rows) { return (rows + 15) & ~15; }
+
+// The four words of scales (16 blocks) from word w0 of a row of `words`.
+template <int VEC>
+__device__ __forceinline__ uint4 load_scale_words(const uint32_t *row, int w0, int words) {
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (VEC == 4) {
+        if (w0 < words) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(row + w0);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        }
+    } else if (VEC == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            if (w0 + i < words) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(row + w0 + i);
+                v[i] = q.x; v[i + 1] = q.y;
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (w0 + i < words) v[i] = row[w0 + i];
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int NUM_A, int BN, int VEC>
+__global__ void __launch_bounds__(kMxThreads, 1)
+    mx4_product_kernel(const __grid_constant__ Mx4Maps maps, const Mx4Args p) {
+    using C = MxCfg<NUM_A, BN>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+    __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][8];
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh, bad_sh;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const volatile int *abort_flag = &abort_sh;
+
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full_bar[s], 2);  // the TMA thread and the scales' warp
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull_bar[a], 1);
+            mbar_init(&tempty_bar[a], 128);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        bad_sh = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&maps.w);
+        tma_prefetch_desc(&maps.a);
+        if (NUM_A == 2) tma_prefetch_desc(&maps.w3);
+    }
+    if (warp == 1) tmem_alloc(&tmem_base_sh, kMxTmemCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = tmem_base_sh;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Inclusive sums over the experts of their rows and of their tiles.  Rows
+    // past p.N do not exist: counts that say otherwise are cut and reported.
+    {
+        constexpr int kWarps = kMxThreads / 32;
+        int carry_r = 0, carry_t = 0;
+        for (int e0 = 0; e0 < p.E; e0 += kMxThreads) {
+            const int e = e0 + tid;
+            const int c = e < p.E ? p.counts[e] : 0;
+            if (c < 0 || c > p.N) bad_sh = 1;
+            int r = c < 0 ? 0 : c > p.N ? p.N : c;
+            long long sum = r;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            // saturate: any sum past N is as good as N + 1 here
+            if (lane == 31) s_warp[0][warp] = int(sum > p.N ? p.N + 1ll : sum);
+            __syncthreads();
+            long long before = carry_r;
+            for (int w = 0; w < warp; ++w) before += s_warp[0][w];
+            const long long end = min(before + sum, (long long)p.N + 1);
+            if (end > p.N) bad_sh = 1;
+            const int hi = int(min(end, (long long)p.N));
+            const int lo = int(min(min(before + sum - r, (long long)p.N), (long long)hi));
+            int t = (hi - lo + BN - 1) / BN;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += v;
+            }
+            if (lane == 31) s_warp[1][warp] = t;
+            __syncthreads();
+            int tb = carry_t;
+            for (int w = 0; w < warp; ++w) tb += s_warp[1][w];
+            if (e < p.E) {
+                s_rows[e] = hi;
+                s_tiles[e] = tb + t;
+            }
+            long long all = carry_r;
+            for (int w = 0; w < kWarps; ++w) {
+                all += s_warp[0][w];
+                carry_t += s_warp[1][w];
+            }
+            carry_r = int(min(all, (long long)p.N + 1));
+            __syncthreads();
+        }
+    }
+    const int n_mb = p.n >> 7;
+    const int n_units = s_tiles[p.E - 1] * n_mb;
+    const int nkb = (p.k + kMxStepK - 1) / kMxStepK;
+
+    if (warp == 0) {
+        // -------------------------------------------- codes, weight scales --
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            const int chunks = p.k >> 7;
+            for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+                const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+                const int w_row = w.e * p.n + w.mb * 128;
+                const long long sf = (long long)(w_row >> 7) * chunks * kMxSfChunk;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = int(it % STAGES);
+                    if (!mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
+                                           p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (p.fault_skip && blockIdx.x == 0 && it == 0)
+                        continue;  // test hook: this stage never fills
+                    uint8_t *st = smem + size_t(s) * C::STAGE_BYTES;
+                    const uint32_t sfb = min(2, chunks - 2 * kb) * kMxSfChunk;
+                    mbar_arrive_expect_tx(&full_bar[s],
+                                          NUM_A * (C::A_BYTES + sfb) + C::B_BYTES);
+                    tma_load_2d(st, &maps.w, kb * 128, w_row, &full_bar[s]);
+                    if (NUM_A == 2)
+                        tma_load_2d(st + C::A_BYTES, &maps.w3, kb * 128, w_row, &full_bar[s]);
+                    tma_load_2d(st + C::OFF_B, &maps.a, kb * 128, w.row, &full_bar[s]);
+                    const long long o = sf + (long long)kb * 2 * kMxSfChunk;
+                    bulk_load(st + C::OFF_SFA, p.w_scales + o, sfb, &full_bar[s]);
+                    if (NUM_A == 2)
+                        bulk_load(st + C::OFF_SFA + C::SFA_BYTES, p.w3_scales + o, sfb,
+                                  &full_bar[s]);
+                }
+            }
+            if (!ok) {
+                *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+                // Let this CTA's own copies land before it can exit.  A stage
+                // whose scales never came does not complete: its wait is bounded.
+                for (uint32_t j = (it > uint32_t(STAGES) ? it - STAGES : 0u); j < it; ++j)
+                    mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
+                                      p.timeout_ns);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer --
+        if (lane == 0) {
+            uint32_t it = 0, lu = 0;
+            bool ok = true;
+            const int chunks = p.k >> 7;
+            for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++lu) {
+                const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+                const int cols = mx_cols(w.rows);
+                const uint32_t a = lu % C::ACC_BUFS;
+                if (!mbar_wait_bounded(&tempty_bar[a], ((lu / C::ACC_BUFS) & 1u) ^ 1u, abort_flag,
+                                       p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d0 = tmem_base + a * C::ACC_COLS;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = int(it % STAGES);
+                    if (!mbar_wait_bounded(&full_bar[s], (it / STAGES) & 1u, abort_flag,
+                                           p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t sa = smem_u32(smem + size_t(s) * C::STAGE_BYTES);
+                    const uint32_t sf =
+                        tmem_base + kMxTmemCols - kMxSfCols + (it & 1u) * C::SF_COLS;
+                    const int nc = min(2, chunks - 2 * kb);
+                    for (int c = 0; c < nc; ++c) {
+                        // columns: [chunk][W, W3, B tiles] x 4
+                        const uint32_t col = sf + c * 4 * (NUM_A + C::B_SF_TILES);
+#pragma unroll
+                        for (int m = 0; m < NUM_A; ++m)
+                            tmem_cp_scales(col + 4 * m,
+                                           sa + C::OFF_SFA + m * C::SFA_BYTES + c * kMxSfChunk);
+#pragma unroll
+                        for (uint32_t j = 0; j < C::B_SF_TILES; ++j)
+                            tmem_cp_scales(col + 4 * (NUM_A + j),
+                                           sa + C::OFF_SFB + (c * C::B_SF_TILES + j) * kMxSfChunk);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t off = (c * 2 + h) * 32;
+                            const uint64_t bdesc = umma_desc_sw128(sa + C::OFF_B + off);
+                            const uint32_t id = mxf4_idesc(cols, 2 * h);
+                            const uint32_t acc = (kb | c | h) ? 1u : 0u;
+#pragma unroll
+                            for (int m = 0; m < NUM_A; ++m)
+                                umma_mxf4(d0 + m * BN, umma_desc_sw128(sa + m * C::A_BYTES + off),
+                                          bdesc, id, col + 4 * m, col + 4 * NUM_A, acc);
+                        }
+                    }
+                    umma_commit(&empty_bar[s]);
+                }
+                if (!ok) break;
+                umma_commit(&tfull_bar[a]);
+            }
+            if (!ok) {
+                *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+                umma_commit(&drain_bar);  // wait for what was issued
+                mbar_wait_bounded(&drain_bar, 0u, nullptr, p.timeout_ns);
+            }
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------ token rows' scales --
+        // One step = 16 blocks of k = two stages; lane l carries rows l, l +
+        // 32, ..., and the words of a chunk are exactly its 16 bytes there.
+        constexpr int RPL = (BN + 31) / 32;
+        const int words = p.k >> 7;  // 32-bit words of scales per row
+        const uint32_t *base = reinterpret_cast<const uint32_t *>(p.a_scales);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+            uint4 next[RPL];
+            auto load = [&](int step) {
+#pragma unroll
+                for (int q = 0; q < RPL; ++q) {
+                    const int r = lane + 32 * q;
+                    next[q] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < w.rows)
+                        next[q] = load_scale_words<VEC>(base + (long long)(w.row + r) * words,
+                                                        step * 4, words);
+                }
+            };
+            load(0);
+            for (int step = 0; step * 2 < nkb && ok; ++step) {
+                uint4 cur[RPL];
+#pragma unroll
+                for (int q = 0; q < RPL; ++q) cur[q] = next[q];
+                if ((step + 1) * 2 < nkb) load(step + 1);
+                for (int h = 0; h < 2 && step * 2 + h < nkb; ++h, ++it) {
+                    const int s = int(it % STAGES);
+                    ok = mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
+                                           p.timeout_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t *sfb = smem + size_t(s) * C::STAGE_BYTES + C::OFF_SFB;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (uint32_t j = 0; j < C::B_SF_TILES; ++j) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int rq = int(j) * 4 + q;
+                                v[q] = 0u;
+                                if (rq < RPL) {
+                                    const uint4 x = cur[rq < RPL ? rq : 0];
+                                    v[q] = h ? (c ? x.w : x.z) : (c ? x.y : x.x);
+                                }
+                            }
+                            *reinterpret_cast<uint4 *>(sfb + (c * C::B_SF_TILES + j) * kMxSfChunk +
+                                                       lane * 16) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    // the tensor core reads them through the async proxy
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full_bar[s]);
+                }
+            }
+        }
+        if (!ok && lane == 0) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+    } else {
+        // -------------------------------------------------------- epilogue --
+        const int q = warp & 3;  // TMEM lane quadrant of this warp
+        uint32_t lu = 0;
+        for (int u = blockIdx.x; u < n_units; u += gridDim.x, ++lu) {
+            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+            const uint32_t a = lu % C::ACC_BUFS;
+            bool ok = mbar_wait_bounded(&tfull_bar[a], (lu / C::ACC_BUFS) & 1u, abort_flag,
+                                        p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + a * C::ACC_COLS;
+            const long long at = (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
+#pragma unroll 1
+            for (int c0 = 0; c0 < w.rows; c0 += 16) {
+                uint32_t g[16], v[16];
+                tmem_ld_16(tb + c0, g);
+                if (NUM_A == 2) tmem_ld_16(tb + BN + c0, v);
+                tmem_ld_wait();
+                reg_fence_16(g);
+                if (NUM_A == 2) reg_fence_16(v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    if (c0 + c >= w.rows) continue;
+                    float y = __uint_as_float(g[c]);
+                    if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
+                    const long long o = at + (long long)(c0 + c) * p.n;
+                    if (p.out_f32)
+                        static_cast<float *>(p.out)[o] = y;
+                    else
+                        static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(y);
+                }
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&tempty_bar[a]);
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+        // Own word of this CTA: no other call's or CTA's status can meet it.
+        p.status[64 + blockIdx.x] =
+            abort_sh ? int(DEV_ERR_TIMEOUT) : bad_sh ? int(DEV_ERR_INTERNAL) : int(DEV_OK);
+        if (blockIdx.x == 0) p.status[0] = int(gridDim.x);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, kMxTmemCols);
+    }
+}
+
+template <int NUM_A, int BN, int VEC>
+cudaError_t launch_product_vec(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
+    using C = MxCfg<NUM_A, BN>;
+    auto kern = mx4_product_kernel<NUM_A, BN, VEC>;
+    static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
+    cudaError_t e = set_smem_once(kern, int(C::SMEM_BYTES), attr_set);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(kMxThreads), C::SMEM_BYTES, st, maps, a);
+}
+
+template <int NUM_A, int BN>
+cudaError_t launch_product(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
+    const int words = a.k >> 7;  // widest load every row's scales are aligned to
+    if (words % 4 == 0) return launch_product_vec<NUM_A, BN, 4>(maps, a, grid, st);
+    if (words % 2 == 0) return launch_product_vec<NUM_A, BN, 2>(maps, a, grid, st);
+    return launch_product_vec<NUM_A, BN, 1>(maps, a, grid, st);
+}
+
+// Token rows per tile, from the mean rows per expert a full batch would have.
+int product_bn(int N, int E) {
+    const long long avg = ((long long)N + E - 1) / E;
+    return avg <= 16 ? 32 : avg <= 64 ? 64 : 128;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+constexpr size_t kMxWorkspace = 8192;  // status words: [0] CTAs, [64 + b] CTA b
+constexpr int kMxMaxCtas = 1024;
+
+beam_status check_mx4_desc(const beam_mx4_desc *d) {
+    if (!d) return BEAM_ERR_INVALID_ARG;
+    if (d->N < 0 || d->E <= 0 || d->E > kMaxE || d->n <= 0 || d->k <= 0) return BEAM_ERR_INVALID_ARG;
+    if (d->swiglu != 0 && d->swiglu != 1) return BEAM_ERR_INVALID_ARG;
+    if (d->out_dtype != BEAM_BF16 && d->out_dtype != BEAM_F32) return BEAM_ERR_INVALID_ARG;
+    if (d->n % 128 != 0 || d->k % 128 != 0) return BEAM_ERR_UNSUPPORTED_SHAPE;
+    // weight rows are 32-bit TMA coordinates, units 32-bit counters
+    if ((long long)d->E * d->n > 0x7fffffffll) return BEAM_ERR_UNSUPPORTED_SHAPE;
+    if (((long long)d->N / 16 + d->E) * (d->n / 128) > 0x3fffffffll || d->N > 0x3fffffff)
+        return BEAM_ERR_UNSUPPORTED_SHAPE;
+    return BEAM_OK;
+}
+
+beam_status check_rows(int dtype, long long rows, int cols, int tiled) {
+    if (dtype != BEAM_BF16 && dtype != BEAM_F32) return BEAM_ERR_INVALID_ARG;
+    if (rows < 0 || cols <= 0 || (tiled != 0 && tiled != 1)) return BEAM_ERR_INVALID_ARG;
+    if (cols % 32 != 0) return BEAM_ERR_UNSUPPORTED_SHAPE;
+    if (rows > 0x7fffffffffffll / cols) return BEAM_ERR_UNSUPPORTED_SHAPE;
+    if (tiled && (rows % 128 != 0 || cols % 128 != 0)) return BEAM_ERR_UNSUPPORTED_SHAPE;
+    return BEAM_OK;
+}
+
+int rows_grid(long long rows, int cols) {
+    const long long blocks = (rows * (cols / 8) + 255) / 256;
+    const long long most = 8ll * device_sm_count();  // 2048 threads per SM
+    return int(blocks < most ? blocks : most);
+}
+
+}  // namespace
+}  // namespace beam
+
+using namespace beam;
+
+extern "C" {
+
+beam_status beam_mx4_quantize(int dtype, long long rows, int cols, const void *x,
+                              const int32_t *n_rows, uint8_t *codes, uint8_t *scales, int tiled,
+                              void *stream) {
+    beam_status s = check_rows(dtype, rows, cols, tiled);
+    if (s != BEAM_OK) return s;
+    if (tiled && n_rows) return BEAM_ERR_INVALID_ARG;
+    if (rows == 0) return BEAM_OK;
+    if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
+        return BEAM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(n_rows) & 3u) return BEAM_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid(rows_grid(rows, cols)), block(256);
+    uint32_t *out = reinterpret_cast<uint32_t *>(codes);
+    cudaError_t e =
+        dtype == BEAM_BF16
+            ? launch_pdl(mx4_quantize_kernel<__nv_bfloat16>, grid, block, 0, st,
+                         static_cast<const __nv_bfloat16 *>(x), rows, cols, n_rows, out, scales, tiled)
+            : launch_pdl(mx4_quantize_kernel<float>, grid, block, 0, st,
+                         static_cast<const float *>(x), rows, cols, n_rows, out, scales, tiled);
+    return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+}
+
+beam_status beam_mx4_dequantize(int dtype, long long rows, int cols, const uint8_t *codes,
+                                const uint8_t *scales, int tiled, void *out, void *stream) {
+    beam_status s = check_rows(dtype, rows, cols, tiled);
+    if (s != BEAM_OK) return s;
+    if (rows == 0) return BEAM_OK;
+    if (!out || !codes || !scales || !aligned16(out) || !aligned16(codes) || !aligned16(scales))
+        return BEAM_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid(rows_grid(rows, cols)), block(256);
+    const uint32_t *in = reinterpret_cast<const uint32_t *>(codes);
+    cudaError_t e = dtype == BEAM_BF16
+                        ? launch_pdl(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, st, in,
+                                     scales, rows, cols, tiled, static_cast<__nv_bfloat16 *>(out))
+                        : launch_pdl(mx4_dequantize_kernel<float>, grid, block, 0, st, in, scales,
+                                     rows, cols, tiled, static_cast<float *>(out));
+    return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+}
+
+size_t beam_mx4_workspace_size(const beam_mx4_desc *desc) {
+    return check_mx4_desc(desc) == BEAM_OK ? kMxWorkspace : 0;
+}
+
+beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_codes,
+                                    const uint8_t *a_scales, const int32_t *expert_counts,
+                                    const uint8_t *w_codes, const uint8_t *w_scales,
+                                    const uint8_t *w3_codes, const uint8_t *w3_scales, void *out,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    beam_status s = check_mx4_desc(desc);
+    if (s != BEAM_OK) return s;
+    if (!expert_counts || !w_codes || !w_scales) return BEAM_ERR_INVALID_ARG;
+    if (desc->swiglu ? (!w3_codes || !w3_scales) : (w3_codes || w3_scales))
+        return BEAM_ERR_INVALID_ARG;
+    for (const void *q : {static_cast<const void *>(a_codes), static_cast<const void *>(a_scales),
+                          static_cast<const void *>(expert_counts),
+                          static_cast<const void *>(w_codes), static_cast<const void *>(w_scales),
+                          static_cast<const void *>(w3_codes),
+                          static_cast<const void *>(w3_scales), static_cast<const void *>(out)})
+        if (!aligned16(q)) return BEAM_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < kMxWorkspace)
+        return BEAM_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (desc->N == 0)
+        return cudaMemsetAsync(workspace, 0, 256, st) == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+    if (!a_codes || !a_scales || !out) return BEAM_ERR_INVALID_ARG;
+    const int bn = product_bn(desc->N, desc->E);
+    const unsigned long long row_bytes = desc->k / 2, w_rows = (unsigned long long)desc->E * desc->n;
+    Mx4Maps maps;
+    if (!make_byte_tmap(&maps.w, w_codes, row_bytes, w_rows, 128) ||
+        !make_byte_tmap(&maps.w3, desc->swiglu ? w3_codes : w_codes, row_bytes, w_rows, 128) ||
+        !make_byte_tmap(&maps.a, a_codes, row_bytes, desc->N, unsigned(bn)))
+        return BEAM_ERR_CUDA;
+    Mx4Args a;
+    a.N = desc->N;
+    a.E = desc->E;
+    a.n = desc->n;
+    a.k = desc->k;
+    a.out_f32 = desc->out_dtype == BEAM_F32;
+    a.counts = expert_counts;
+    a.a_scales = a_scales;
+    a.w_scales = w_scales;
+    a.w3_scales = w3_scales;
+    a.out = out;
+    a.status = static_cast<int *>(workspace);
+    a.timeout_ns = device_wait_limit_ns();
+    a.fault_skip = device_fault_mode() == FAULT_MX4_STAGE;
+    // No more CTAs than units there can be: a tile per full BN rows plus one
+    // unfilled per expert that has rows.
+    const long long tiles = desc->N / bn + (desc->N < desc->E ? desc->N : desc->E);
+    long long grid = tiles * (desc->n / 128);
+    const int n_sm = device_sm_count() < kMxMaxCtas ? device_sm_count() : kMxMaxCtas;
+    if (grid > n_sm) grid = n_sm;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (desc->swiglu) {
+        if (bn == 32) e = launch_product<2, 32>(maps, a, int(grid), st);
+        if (bn == 64) e = launch_product<2, 64>(maps, a, int(grid), st);
+        if (bn == 128) e = launch_product<2, 128>(maps, a, int(grid), st);
+    } else {
+        if (bn == 32) e = launch_product<1, 32>(maps, a, int(grid), st);
+        if (bn == 64) e = launch_product<1, 64>(maps, a, int(grid), st);
+        if (bn == 128) e = launch_product<1, 128>(maps, a, int(grid), st);
+    }
+    return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+}
+
+beam_status beam_mx4_check(const beam_mx4_desc *desc, void *workspace, void *stream) {
+    beam_status s = check_mx4_desc(desc);
+    if (s != BEAM_OK) return s;
+    if (!workspace) return BEAM_ERR_WORKSPACE;
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return BEAM_ERR_CUDA;
+    int words[64 + kMxMaxCtas];
+    if (cudaMemcpy(words, workspace, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return BEAM_ERR_CUDA;
+    const int n = words[0] < 0 ? 0 : words[0] > kMxMaxCtas ? kMxMaxCtas : words[0];
+    int worst = DEV_OK;
+    for (int b = 0; b < n; ++b) {
+        if (words[64 + b] == DEV_ERR_TIMEOUT) return BEAM_ERR_TIMEOUT;
+        if (words[64 + b] != DEV_OK) worst = DEV_ERR_INTERNAL;
+    }
+    return worst == DEV_OK ? BEAM_OK : BEAM_ERR_INTERNAL;
+}
+
+}  // extern "C"

@@ -377,6 +377,67 @@ beam_status beam_moe_ep_combine(const beam_moe_desc *desc, const float *y_rows,
                                 const int32_t *topk_idx, const float *topk_w,
                                 const int32_t *pair_pos, void *out, void *stream);
 
+/* ------------------------------------- experts in 4-bit floating point --
+ * The layer's experts with weights and token rows in MXFP4 (OCP Microscaling
+ * Formats v1.0), a quarter of the bf16 weight bytes that bound a decode step;
+ * the pages have no counterpart.  Blocks of 32 consecutive values of a row
+ * share one scale 2^X, X = floor(log2 max|v|) - 2 (at least -127), stored as
+ * the byte X + 127; each value is v / 2^X rounded to nearest, ties to even, on
+ * the E2M1 grid 0, .5, 1, 1.5, 2, 3, 4, 6 with a sign bit, saturating at 6.  A
+ * block that holds an infinity or a NaN stands for NaN throughout: scale byte
+ * 255, codes 0.  codes [rows, cols / 2]: value 2i of a row in the low half of
+ * byte i, value 2i + 1 in the high half.  scales [rows, cols / 32], either row
+ * by row (tiled = 0) or, for the product's weights, in tiles of 128 rows x 4
+ * blocks (tiled = 1; rows and cols % 128 == 0): the byte of (row, block) is at
+ * ((row / 128) (cols / 128) + block / 4) 512 + 16 (row % 32) +
+ * 4 ((row % 128) / 32) + block % 4.
+ * Pointers are 16-byte aligned, cols % 32 == 0.  Rows need no alignment. */
+
+/* x [rows, cols] of `dtype` -> codes, scales.  n_rows (device int32, or NULL):
+ * only the first min(*n_rows, rows) rows are read and written (not with
+ * tiled = 1), so that rows whose number only the device knows need no copy to
+ * the host. */
+beam_status beam_mx4_quantize(int dtype, long long rows, int cols, const void *x,
+                              const int32_t *n_rows, uint8_t *codes, uint8_t *scales, int tiled,
+                              void *stream);
+
+/* The values the codes stand for, in `dtype` (exact: every value of the
+ * format with X <= 125 is a bfloat16). */
+beam_status beam_mx4_dequantize(int dtype, long long rows, int cols, const uint8_t *codes,
+                                const uint8_t *scales, int tiled, void *out, void *stream);
+
+/* Grouped product of one projection: N token rows (capacity) of width k,
+ * grouped by expert in ascending order as beam_moe_ep_dispatch lists them, E
+ * experts (<= 256) of n weight rows; n % 128 == 0, k % 128 == 0.  out_dtype:
+ * beam_dtype of out.  swiglu = 1: two weight matrices, gate and up. */
+typedef struct {
+    int N, E, n, k;
+    int swiglu;    /* 0 or 1 */
+    int out_dtype; /* beam_dtype */
+} beam_mx4_desc;
+
+/* out[i, :] = a_i w_e^T for the rows i of expert e, or with swiglu
+ * SiLU(a_i w_e^T) * (a_i w3_e^T) (Eq. 3); fp32 accumulation, one rounding.
+ *   a_codes [N, k/2], a_scales [N, k/32] row by row
+ *   expert_counts int32 [E] (device): rows of each expert, as beam_moe_route
+ *     writes them; expert e's rows follow those of the experts before it.
+ *     Rows past the last expert's are neither used nor written.  Counts that
+ *     are negative or add up to more than N are cut at N and reported
+ *     (BEAM_ERR_INTERNAL through beam_mx4_check).
+ *   w_codes [E, n, k/2] and w_scales in tiles over the E n rows (tiled = 1);
+ *     w3 the same with swiglu, else NULL.  Experts without rows are not read.
+ *   out [N, n] of out_dtype
+ *   workspace: beam_mx4_workspace_size(desc) bytes, 256-byte aligned; calls
+ *     that may overlap need one each. */
+size_t beam_mx4_workspace_size(const beam_mx4_desc *desc);
+beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_codes,
+                                    const uint8_t *a_scales, const int32_t *expert_counts,
+                                    const uint8_t *w_codes, const uint8_t *w_scales,
+                                    const uint8_t *w3_codes, const uint8_t *w3_scales, void *out,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+/* As beam_moe_check, for the workspace of the last product made on it. */
+beam_status beam_mx4_check(const beam_mx4_desc *desc, void *workspace, void *stream);
+
 /* Synchronise `stream`, then read the workspace error word written by the last
  * call: BEAM_OK, BEAM_ERR_TIMEOUT (a bounded device wait expired, the kernel
  * returned early; that call's outputs are not valid) or BEAM_ERR_INTERNAL (a
@@ -403,7 +464,9 @@ float beam_moe_tau_to_logit(float tau);
  *   mode 2  the same in CTA 0 of the router GEMM of every later route or
  *           forward call (bf16 only);
  *   mode 3  the same in CTA 0 of the shared experts' gate/up GEMM of every
- *           later forward call with shared experts (bf16 only).
+ *           later forward call with shared experts (bf16 only);
+ *   mode 4  the same in CTA 0 of every later beam_mx4_expert_product
+ *           (beam_mx4_check then reports it).
  * The kernels then record the timeout, let their own copies and MMAs land,
  * free their tensor memory and return: beam_moe_check reports
  * BEAM_ERR_TIMEOUT and the context stays usable.  wait_limit_ns replaces the

@@ -1,0 +1,188 @@
+"""The 4-bit floating point operators on the GPU: rows to MXFP4 and back
+against a plain implementation of the format in 64 bits, the grouped product
+against fp64 products of the values the codes stand for, and refusals.
+
+Bars, from the arithmetic: quantising and reading back round nothing but the
+4-bit digits, so codes, scales and values are equal bit for bit.  The product
+accumulates exact products in fp32: each of the k terms adds at most 2^-24 of
+the running sum, bounded by sum |a w|, and some tensor core sums cut rather
+than round, hence k 2^-23 sum|a w|; the bf16 output adds half a step, 2^-9
+relative to a power of two above, 2^-8 of the value.  SwiGLU: SiLU's slope is
+at most 1.1, so an error of dg in the gate and du in the up value moves
+g s(g) u by at most 1.1 dg |u| + |g| du, plus 8 2^-24 of the result for the
+exponential, division and products.
+"""
+import numpy as np
+import pytest
+import torch
+
+from dynamic_expert_routing_router_b200 import abi
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+GRID = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], np.float64)
+
+
+def plain_quantize(x):
+    """(digits' codes, scale bytes) in 64 bits, straight from the format."""
+    x = x.double().cpu().numpy()
+    rows, cols = x.shape
+    v = x.reshape(rows, cols // 32, 32)
+    top = np.abs(v).max(axis=2)
+    bad = ~np.isfinite(top)
+    with np.errstate(divide="ignore"):
+        X = np.where((top > 0) & ~bad, np.floor(np.log2(np.where(bad | (top == 0), 1.0, top))), -125) - 2
+    X = np.maximum(X, -127)
+    a = np.abs(np.where(bad[:, :, None], 0.0, v)) / np.exp2(X)[:, :, None]
+    mid = (GRID[1:] + GRID[:-1]) / 2
+    lo, hi = np.searchsorted(mid, a, side="left"), np.searchsorted(mid, a, side="right")
+    code = np.where(hi % 2 == 0, hi, lo)  # they differ on a tie: the even digit
+    code = code + 8 * np.signbit(v)
+    code = np.where(bad[:, :, None], 0, code).reshape(rows, cols // 2, 2)
+    return ((code[:, :, 0] | (code[:, :, 1] << 4)).astype(np.uint8),
+            np.where(bad, 255, X + 127).astype(np.uint8))
+
+
+def plain_values(codes, scales):
+    c = np.stack([codes & 15, codes >> 4], axis=2).reshape(codes.shape[0], -1)
+    v = np.where(c < 8, 1.0, -1.0) * GRID[c & 7]
+    f = np.exp2(scales.astype(np.float64) - 127)
+    f[scales == 255] = np.nan
+    return v * np.repeat(f, 32, axis=1)
+
+
+def tile_scales(scales):
+    t = scales.reshape(scales.shape[0] // 128, 4, 32, scales.shape[1] // 4, 4)
+    return t.permute(0, 3, 2, 1, 4).contiguous().reshape(scales.shape)
+
+
+def quantize(x, **kw):
+    codes = torch.full((x.shape[0], x.shape[1] // 2), 0xEE, dtype=torch.uint8, device=DEV)
+    scales = torch.full((x.shape[0], x.shape[1] // 32), 0xEE, dtype=torch.uint8, device=DEV)
+    abi.mx4_quantize(x, codes, scales, **kw)
+    return codes, scales
+
+
+def rows_of(rows, cols, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g, device=DEV)
+    return (x * torch.exp(3 * torch.randn(rows, 1, generator=g, device=DEV))).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 96), (129, 2048), (1000, 160)])
+def test_quantize_is_the_format_bit_for_bit(rows, cols, dtype):
+    x = rows_of(rows, cols, dtype, rows + cols)
+    codes, scales = quantize(x)
+    c, s = plain_quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(codes.cpu().numpy(), c)
+    for out in (torch.bfloat16, torch.float32):
+        v = torch.empty(rows, cols, dtype=out, device=DEV)
+        abi.mx4_dequantize(codes, scales, v)
+        assert np.array_equal(v.double().cpu().numpy(), plain_values(c, s))
+
+
+def test_quantize_ties_zeros_extremes_and_non_finite():
+    x = torch.zeros(9, 32, device=DEV)
+    # every digit's neighbourhood and both ties, with 6 (or 4) as the largest
+    t = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.2499, 0.2501, 5.0001, 6.0, 7.9],
+                     device=DEV)
+    x[0, :12] = t
+    x[0, 12:24] = -t
+    x[1, :5] = torch.tensor([1e-45, -1e-45, 1e-40, 0.0, -0.0], device=DEV)  # subnormals
+    x[2, 7] = 3.4e38
+    x[2, 8] = -3.0e38
+    x[3, 3] = float("inf")
+    x[4, 31] = float("nan")
+    x[4, 0] = 1.0
+    x[5, 0] = -0.0
+    x[6, :] = 2.0 ** -126
+    x[7, :] = 2.0 ** -124 * 1.5
+    x[8, 0], x[8, 1] = float("-inf"), float("nan")
+    codes, scales = quantize(x)
+    c, s = plain_quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), c)
+    v = torch.empty_like(x)
+    abi.mx4_dequantize(codes, scales, v)
+    assert np.array_equal(v.double().cpu().numpy(), plain_values(c, s), equal_nan=True)
+    assert torch.isnan(v[3]).all() and torch.isnan(v[4]).all() and (v[5] == 0).all()
+
+
+def test_tiled_scales_and_row_limit():
+    x = rows_of(256, 384, torch.bfloat16, 5)
+    codes, scales = quantize(x)
+    codes_t, scales_t = quantize(x, tiled=True)
+    assert torch.equal(codes, codes_t) and torch.equal(scales_t, tile_scales(scales))
+    v, vt = torch.empty_like(x), torch.empty_like(x)
+    abi.mx4_dequantize(codes, scales, v)
+    abi.mx4_dequantize(codes_t, scales_t, vt, tiled=True)
+    assert torch.equal(v, vt)
+    for n in (0, 1, 77, 256, 1000, -3):
+        c, s = quantize(x, n_rows=torch.tensor([n], dtype=torch.int32, device=DEV))
+        m = min(max(n, 0), 256)
+        assert torch.equal(c[:m], codes[:m]) and torch.equal(s[:m], scales[:m])
+        assert (c[m:] == 0xEE).all() and (s[m:] == 0xEE).all()
+
+
+# ------------------------------------------------------------- product --
+
+def operands(counts, n, k, seed, swiglu=False, tail=0):
+    E, P = len(counts), sum(counts)
+    a = quantize(rows_of(P + tail, k, torch.float32, seed)) if P + tail else (
+        torch.empty(0, k // 2, dtype=torch.uint8, device=DEV),
+        torch.empty(0, k // 32, dtype=torch.uint8, device=DEV))
+    ws = [quantize(rows_of(E * n, k, torch.float32, seed + 1 + i)) for i in range(2 if swiglu else 1)]
+    return a, ws
+
+
+def product(counts, n, k, a, ws, out="f32", stream=None, N=None):
+    E, N = len(counts), a[0].shape[0] if N is None else N
+    dsc = abi.mx4_desc(N, E, n, k, swiglu=len(ws) == 2, out=out)
+    wk = abi.alloc_mx4_workspace(dsc)
+    y = torch.full((N, n), 7.0, dtype=torch.float32 if out == "f32" else torch.bfloat16, device=DEV)
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    kw = dict(w3_codes=ws[1][0], w3_scales=tile_scales(ws[1][1])) if len(ws) == 2 else {}
+    abi.mx4_expert_product(dsc, *a, c, ws[0][0], tile_scales(ws[0][1]), y, wk, **kw)
+    return y, dsc, wk
+
+
+def assert_product(y, counts, n, k, a, ws, out):
+    A = plain_values(a[0].cpu().numpy(), a[1].cpu().numpy())
+    W = [plain_values(w[0].cpu().numpy(), w[1].cpu().numpy()).reshape(len(counts), n, k) for w in ws]
+    y = y.double().cpu().numpy()
+    r = 0
+    eps = k * 2.0 ** -23
+    for e, m in enumerate(counts):
+        if m == 0:
+            continue
+        rows = A[r:r + m]
+        g, dg = rows @ W[0][e].T, eps * (np.abs(rows) @ np.abs(W[0][e]).T)
+        ref, tol = g, dg
+        if len(ws) == 2:
+            u, du = rows @ W[1][e].T, eps * (np.abs(rows) @ np.abs(W[1][e]).T)
+            ref = g / (1 + np.exp(-g)) * u
+            tol = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + 8 * 2.0 ** -24 * np.abs(ref)
+        if out == "bf16":
+            tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        bad = np.abs(y[r:r + m] - ref) > tol + 1e-37
+        assert not bad.any(), (e, m, int(bad.sum()), np.argwhere(bad)[:4].tolist(),
+                               float(np.abs(y[r:r + m] - ref).max()))
+        r += m
+    assert (y[r:] == 7.0).all(), "rows behind the last expert's were written"
+
+
+SIZES = [([1], 128, 128), ([5, 0, 3], 128, 256), ([0, 17, 1, 33], 256, 384), ([130, 2], 384, 640),
+         ([300], 128, 1024), ([0, 0, 0, 0, 9], 640, 768)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("counts,n,k", SIZES, ids=[f"{sum(c)}x{n}x{k}" for c, n, k in SIZES])
+def test_product_matches_fp64(counts, n, k, swiglu, out):
+    a, ws = operands(counts, n, k, seed=n + k, swiglu=swiglu, tail=3)
+    if swiglu:  # keep exp(-g) far from overflow: the bound above is relative
+        a = (a[0], a[1].clamp(max=127))
+    y, dsc, wk = product(counts, n, k, a, ws, out)
+    abi.mx4_check(dsc, wk)
+    assert_product(y, counts, n, k, a, ws, out)

@@ -40,6 +40,19 @@ class Mx4Desc(ctypes.Structure):
                 ("k", ctypes.c_int), ("swiglu", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
+class BlockDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("accumulate", ctypes.c_int)]
+
+
+class BalanceDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("E", ctypes.c_int), ("K", ctypes.c_int),
+                ("n_seq", ctypes.c_int), ("logits_ld", ctypes.c_int), ("has_mask", ctypes.c_int),
+                ("count_kept", ctypes.c_int), ("mask_logit_threshold", ctypes.c_float),
+                ("coef", ctypes.c_float)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("BN", ctypes.c_int), ("router_bn", ctypes.c_int),
                 ("router_splits", ctypes.c_int), ("p_cap", ctypes.c_int),
@@ -89,6 +102,9 @@ def lib():
         L.beam_moe_backward.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
                                         vp, vp, vp, vp, sz, vp]
         L.beam_moe_backward.restype = i32
+        L.beam_moe_backward_aux.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp,
+                                            vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_backward_aux.restype = i32
         L.beam_moe_backward_kernel_count.argtypes = [pd]
         L.beam_moe_backward_kernel_count.restype = i32
         L.beam_moe_ep_dispatch.argtypes = [pd, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -103,6 +119,21 @@ def lib():
         L.beam_moe_tau_to_logit.restype = ctypes.c_float
         L.beam_moe_set_fault_injection.argtypes = [i32, ctypes.c_ulonglong]
         L.beam_moe_set_fault_injection.restype = i32
+        pb = ctypes.POINTER(BlockDesc)
+        L.beam_block_enter.argtypes = [pb, vp, vp, vp, vp]
+        L.beam_block_exit.argtypes = [pb, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.beam_block_workspace_size.argtypes = [pb]
+        L.beam_block_workspace_size.restype = sz
+        L.beam_block_enter_backward.argtypes = [pb, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_block_exit_backward.argtypes = [pb] + [vp] * 15 + [sz, vp]
+        pl = ctypes.POINTER(BalanceDesc)
+        L.beam_moe_balance_workspace_size.argtypes = [pl]
+        L.beam_moe_balance_workspace_size.restype = sz
+        L.beam_moe_balance.argtypes = [pl, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_balance_backward.argtypes = [pl, vp, vp, vp, vp, vp, vp]
+        for f in ("beam_block_enter", "beam_block_exit", "beam_block_enter_backward",
+                  "beam_block_exit_backward", "beam_moe_balance", "beam_moe_balance_backward"):
+            getattr(L, f).restype = i32
         i64 = ctypes.c_longlong
         L.beam_mx4_quantize.argtypes = [i32, i64, i32, vp, vp, vp, vp, i32, vp]
         L.beam_mx4_dequantize.argtypes = [i32, i64, i32, vp, vp, i32, vp, vp]
@@ -202,10 +233,22 @@ def alloc_backward_workspace(dsc: Desc, device=None):
 
 
 def backward(dsc, x, W_gate, W_mask, W1, W3, W2, dy, beta, dx, dW_gate, dW_mask, dW1, dW3, dW2,
-             workspace, stream=None):
+             workspace, stream=None, dlogits=None):
     """Training-mode gradients (straight-through estimator, beta-weighted
     penalty on the candidates' mask scores).  dx is overwritten; the weight
-    gradients (fp32, shaped like their weights) are accumulated into."""
+    gradients (fp32, shaped like their weights) are accumulated into.
+    dlogits: a further gradient of the main router's logits, f32 [T, E]
+    (balance_backward), that goes on to dx and dW_gate."""
+    if dlogits is not None:
+        import torch
+        aux = _arg("beam_moe_backward_aux", "dlogits", dlogits, torch.float32, (dsc.T, dsc.E),
+                   _current_device())
+        _ok(lib().beam_moe_backward_aux(
+            ctypes.byref(dsc), _ptr(x), _ptr(W_gate), _ptr(W_mask), _ptr(W1), _ptr(W3), _ptr(W2),
+            _ptr(dy), aux, ctypes.c_float(beta), _ptr(dx), _ptr(dW_gate), _ptr(dW_mask),
+            _ptr(dW1), _ptr(dW3), _ptr(dW2), _ptr(workspace), workspace.numel(),
+            _stream(stream)), "beam_moe_backward_aux")
+        return
     _ok(lib().beam_moe_backward(ctypes.byref(dsc), _ptr(x), _ptr(W_gate), _ptr(W_mask),
                                 _ptr(W1), _ptr(W3), _ptr(W2), _ptr(dy), ctypes.c_float(beta),
                                 _ptr(dx), _ptr(dW_gate), _ptr(dW_mask), _ptr(dW1), _ptr(dW3),
@@ -330,9 +373,10 @@ def _torch_dtype(code):
     return torch.bfloat16 if code == BEAM_BF16 else torch.float32
 
 
-def _arg(what, name, t, dtype, shape, optional=False):
+def _arg(what, name, t, dtype, shape, dev, optional=False):
     """The address of tensor `t`, which has to be a contiguous `dtype` tensor
-    of `shape` on the current device; None where it may be left out."""
+    of `shape` on device `dev` (_current_device()); None where it may be left
+    out."""
     if t is None:
         if optional:
             return None
@@ -340,19 +384,192 @@ def _arg(what, name, t, dtype, shape, optional=False):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise BeamError(1, f"{what}: {name} has to be a contiguous {dtype} tensor of shape "
                            f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device.type != "cuda" or t.device.index != _current_device():
+    if t.get_device() != dev:
         raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
     return t.data_ptr()
 
 
-def _current_device():
+def _workspace(what, t, dev):
+    """(address, bytes) of a uint8 workspace on device `dev`."""
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if t is None:
+        raise BeamError(3, f"{what}: the workspace is missing")
+    return _arg(what, "workspace", t, torch.uint8, t.shape, dev), t.numel()
+
+
+def _alloc(what, n, device):
+    import torch
+    if n == 0:
+        raise BeamError(1, what)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _current_device():
+    """Index of the current CUDA device.  Before CUDA is up no tensor can be on
+    one: -2, which no tensor's get_device() gives."""
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _stream_on(stream, dev):
+    """Raw handle of `stream`, by default the current one of device `dev`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+# ------------------------------------------------- the residual block around --
+
+def block_desc(T, d, dtype="bf16", eps=1e-6, res_scale=1.0, branch_scale=1.0,
+               accumulate=False) -> BlockDesc:
+    """T rows of width d around the layer; out = res_scale res + branch_scale
+    (gated, normed y).  accumulate: the backward adds to the weights' gradients."""
+    return BlockDesc(int(T), int(d), _code(dtype), float(eps), float(res_scale),
+                     float(branch_scale), int(accumulate))
+
+
+def block_workspace_size(dsc: BlockDesc) -> int:
+    return int(lib().beam_block_workspace_size(ctypes.byref(dsc)))
+
+
+def alloc_block_workspace(dsc: BlockDesc, device=None):
+    """A uint8 torch tensor of block_workspace_size(dsc) bytes on `device`."""
+    return _alloc("beam_block_workspace_size", block_workspace_size(dsc), device)
+
+
+def block_enter(dsc, x, w, n, stream=None):
+    """n = x r(x) w, r(x) = 1 / sqrt(mean x^2 + eps) per row: what the layer reads."""
+    what, dt, dev = "beam_block_enter", _torch_dtype(dsc.dtype), _current_device()
+    rows, row = (dsc.T, dsc.d), (dsc.d,)
+    _ok(lib().beam_block_enter(dsc, _arg(what, "x", x, dt, rows, dev),
+                               _arg(what, "w", w, dt, row, dev),
+                               _arg(what, "n", n, dt, rows, dev), _stream_on(stream, dev)), what)
+
+
+def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=None, n_next=None,
+               stream=None):
+    """out = res_scale res + branch_scale sigmoid(gate_t) gate_c w_out y r(y)
+    (each of w_out [d], gate_c [d], gate_t [T] may be left out; without w_out y
+    is not normed); with w_next also n_next = out r(out) w_next."""
+    what, dt, dev = "beam_block_exit", _torch_dtype(dsc.dtype), _current_device()
+    rows, row = (dsc.T, dsc.d), (dsc.d,)
+    if (w_next is None) != (n_next is None):
+        raise BeamError(1, f"{what}: w_next and n_next go together")
+    _ok(lib().beam_block_exit(
+        dsc, _arg(what, "res", res, dt, rows, dev), _arg(what, "y", y, dt, rows, dev),
+        _arg(what, "w_out", w_out, dt, row, dev, True),
+        _arg(what, "gate_c", gate_c, dt, row, dev, True),
+        _arg(what, "gate_t", gate_t, dt, (dsc.T,), dev, True),
+        _arg(what, "out", out, dt, rows, dev), _arg(what, "w_next", w_next, dt, row, dev, True),
+        _arg(what, "n_next", n_next, dt, rows, dev, True), _stream_on(stream, dev)), what)
+
+
+def block_enter_backward(dsc, x, w, dn, dx, dw, workspace, dskip=None, stream=None):
+    """dx = dskip + dn (f32, as backward's dx) through the norm; dw f32 [d]."""
+    import torch
+    what, dt, dev = "beam_block_enter_backward", _torch_dtype(dsc.dtype), _current_device()
+    rows, row, f32 = (dsc.T, dsc.d), (dsc.d,), torch.float32
+    ws, n = _workspace(what, workspace, dev)
+    _ok(lib().beam_block_enter_backward(
+        dsc, _arg(what, "x", x, dt, rows, dev), _arg(what, "w", w, dt, row, dev),
+        _arg(what, "dn", dn, f32, rows, dev), _arg(what, "dskip", dskip, dt, rows, dev, True),
+        _arg(what, "dx", dx, dt, rows, dev), _arg(what, "dw", dw, f32, row, dev), ws, n,
+        _stream_on(stream, dev)), what)
+
+
+def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=None, w_out=None,
+                        gate_c=None, gate_t=None, w_next=None, dw_out=None, dgate_c=None,
+                        dgate_t=None, dw_next=None, stream=None):
+    """Gradients of block_exit for dout and, with w_next, dn_next (f32): dres
+    and dy in the rows' dtype, and in f32 that of each weight and gate that is
+    given (dw_out, dgate_c, dw_next [d], dgate_t [T])."""
+    import torch
+    what, dt, dev = "beam_block_exit_backward", _torch_dtype(dsc.dtype), _current_device()
+    rows, row, toks, f32 = (dsc.T, dsc.d), (dsc.d,), (dsc.T,), torch.float32
+    for name, a, b in (("w_out", w_out, dw_out), ("gate_c", gate_c, dgate_c),
+                       ("gate_t", gate_t, dgate_t), ("w_next", w_next, dw_next),
+                       ("w_next", w_next, dn_next)):
+        if (a is None) != (b is None):
+            raise BeamError(1, f"{what}: {name} and its gradient go together")
+    ws, n = _workspace(what, workspace, dev)
+    _ok(lib().beam_block_exit_backward(
+        dsc, _arg(what, "y", y, dt, rows, dev),
+        _arg(what, "out", out, dt, rows, dev, w_next is None),
+        _arg(what, "w_out", w_out, dt, row, dev, True),
+        _arg(what, "gate_c", gate_c, dt, row, dev, True),
+        _arg(what, "gate_t", gate_t, dt, toks, dev, True),
+        _arg(what, "w_next", w_next, dt, row, dev, True),
+        _arg(what, "dout", dout, dt, rows, dev),
+        _arg(what, "dn_next", dn_next, f32, rows, dev, True),
+        _arg(what, "dres", dres, dt, rows, dev), _arg(what, "dy", dy, dt, rows, dev),
+        _arg(what, "dw_out", dw_out, f32, row, dev, True),
+        _arg(what, "dgate_c", dgate_c, f32, row, dev, True),
+        _arg(what, "dgate_t", dgate_t, f32, toks, dev, True),
+        _arg(what, "dw_next", dw_next, f32, row, dev, True), ws, n, _stream_on(stream, dev)),
+        what)
+
+
+# ------------------------------------------------------------ balance loss --
+
+def balance_desc(T, E, K, n_seq=1, logits_ld=None, has_mask=False, count_kept=False, tau=0.5,
+                 coef=1.0) -> BalanceDesc:
+    """Balance loss over n_seq sequences of T tokens in all.  logits_ld: floats
+    per row of the logits (default E, or 2 E with has_mask: route's)."""
+    ld = (2 * E if has_mask else E) if logits_ld is None else logits_ld
+    return BalanceDesc(int(T), int(E), int(K), int(n_seq), int(ld), int(has_mask),
+                       int(count_kept), tau_logit(tau), float(coef))
+
+
+def balance_workspace_size(dsc: BalanceDesc) -> int:
+    return int(lib().beam_moe_balance_workspace_size(ctypes.byref(dsc)))
+
+
+def alloc_balance_workspace(dsc: BalanceDesc, device=None):
+    """A uint8 torch tensor of balance_workspace_size(dsc) bytes on `device`."""
+    return _alloc("beam_moe_balance_workspace_size", balance_workspace_size(dsc), device)
+
+
+def balance(dsc, logits, loss, cand_counts, workspace, kept_counts=None, mean_prob=None,
+            seq_begin=None, stream=None):
+    """loss f32 [1] = coef / n_seq sum_s sum_e f_se P_se from logits f32
+    [T, logits_ld]; cand_counts (kept_counts) int32 [n_seq, E]: how many tokens
+    of a sequence have (keep) expert e among their K candidates; mean_prob f32
+    [n_seq, E] = P.  seq_begin int32 [n_seq + 1] (device)."""
+    import torch
+    what, dev, i32 = "beam_moe_balance", _current_device(), torch.int32
+    table = (dsc.n_seq, dsc.E)
+    if kept_counts is not None and not dsc.has_mask:
+        raise BeamError(1, f"{what}: kept_counts without a mask")
+    ws, n = _workspace(what, workspace, dev)
+    _ok(lib().beam_moe_balance(
+        dsc, _arg(what, "logits", logits, torch.float32, (dsc.T, dsc.logits_ld), dev),
+        _arg(what, "seq_begin", seq_begin, i32, (dsc.n_seq + 1,), dev, dsc.n_seq == 1),
+        _arg(what, "loss", loss, torch.float32, (1,), dev),
+        _arg(what, "cand_counts", cand_counts, i32, table, dev),
+        _arg(what, "kept_counts", kept_counts, i32, table, dev, True),
+        _arg(what, "mean_prob", mean_prob, torch.float32, table, dev, True), ws, n,
+        _stream_on(stream, dev)), what)
+
+
+def balance_backward(dsc, logits, counts, dlogits, seq_begin=None, dloss=None, stream=None):
+    """dlogits f32 [T, E] of the balance loss, times dloss f32 [1] (device; 1 if
+    left out).  counts: the forward's cand_counts, or kept_counts with
+    count_kept.  backward(..., dlogits=) carries it on."""
+    import torch
+    what, dev = "beam_moe_balance_backward", _current_device()
+    f32, i32 = torch.float32, torch.int32
+    _ok(lib().beam_moe_balance_backward(
+        dsc, _arg(what, "logits", logits, f32, (dsc.T, dsc.logits_ld), dev),
+        _arg(what, "seq_begin", seq_begin, i32, (dsc.n_seq + 1,), dev, dsc.n_seq == 1),
+        _arg(what, "counts", counts, i32, (dsc.n_seq, dsc.E), dev),
+        _arg(what, "dloss", dloss, f32, (1,), dev, True),
+        _arg(what, "dlogits", dlogits, f32, (dsc.T, dsc.E), dev), _stream_on(stream, dev)), what)
 
 
 # ------------------------------------------- experts in 4-bit floating point --
 
-def _mx4_rows(what, x, codes, scales):
+def _mx4_rows(what, x, codes, scales, dev):
     import torch
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
         raise BeamError(1, f"{what}: a bf16 or f32 matrix is wanted, got {x.dtype} "
@@ -361,9 +578,9 @@ def _mx4_rows(what, x, codes, scales):
     if cols % 32:
         raise BeamError(2, f"{what}: {cols} columns are no multiple of 32")
     code = BEAM_BF16 if x.dtype == torch.bfloat16 else BEAM_F32
-    return (code, rows, cols, _arg(what, "values", x, x.dtype, (rows, cols)),
-            _arg(what, "codes", codes, torch.uint8, (rows, cols // 2)),
-            _arg(what, "scales", scales, torch.uint8, (rows, cols // 32)))
+    return (code, rows, cols, _arg(what, "values", x, x.dtype, (rows, cols), dev),
+            _arg(what, "codes", codes, torch.uint8, (rows, cols // 2), dev),
+            _arg(what, "scales", scales, torch.uint8, (rows, cols // 32), dev))
 
 
 def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
@@ -372,17 +589,19 @@ def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
     reads its weights' from.  n_rows: int32 [1] on the device, the rows that
     are there (the others are left as they are)."""
     import torch
-    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_quantize", x, codes, scales)
-    pn = _arg("beam_mx4_quantize", "n_rows", n_rows, torch.int32, (1,), optional=True)
-    _ok(lib().beam_mx4_quantize(code, rows, cols, px, pn, pc, ps, int(tiled), _stream(stream)),
-        "beam_mx4_quantize")
+    dev = _current_device()
+    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_quantize", x, codes, scales, dev)
+    pn = _arg("beam_mx4_quantize", "n_rows", n_rows, torch.int32, (1,), dev, True)
+    _ok(lib().beam_mx4_quantize(code, rows, cols, px, pn, pc, ps, int(tiled),
+                                _stream_on(stream, dev)), "beam_mx4_quantize")
 
 
 def mx4_dequantize(codes, scales, out, tiled=False, stream=None):
     """The values of an MXFP4 matrix, out [rows, cols] bf16 or f32."""
-    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_dequantize", out, codes, scales)
-    _ok(lib().beam_mx4_dequantize(code, rows, cols, pc, ps, int(tiled), px, _stream(stream)),
-        "beam_mx4_dequantize")
+    dev = _current_device()
+    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_dequantize", out, codes, scales, dev)
+    _ok(lib().beam_mx4_dequantize(code, rows, cols, pc, ps, int(tiled), px,
+                                  _stream_on(stream, dev)), "beam_mx4_dequantize")
 
 
 def mx4_desc(N, E, n, k, swiglu=False, out="bf16") -> Mx4Desc:
@@ -397,11 +616,7 @@ def mx4_workspace_size(dsc: Mx4Desc) -> int:
 
 def alloc_mx4_workspace(dsc: Mx4Desc, device=None):
     """A uint8 torch tensor of mx4_workspace_size(dsc) bytes on `device`."""
-    import torch
-    n = mx4_workspace_size(dsc)
-    if n == 0:
-        raise BeamError(1, "beam_mx4_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _alloc("beam_mx4_workspace_size", mx4_workspace_size(dsc), device).zero_()
 
 
 def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, workspace,
@@ -415,17 +630,17 @@ def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, w
     wc, ws = (E * n, k // 2), (E * n, k // 32)
     if dsc.swiglu == 0 and (w3_codes is not None or w3_scales is not None):
         raise BeamError(1, f"{what}: a second weight without swiglu")
-    second = dsc.swiglu != 0
+    second, dev = dsc.swiglu != 0, _current_device()
+    ws_at, ws_n = _workspace(what, workspace, dev)
     _ok(lib().beam_mx4_expert_product(
-        ctypes.byref(dsc), _arg(what, "a_codes", a_codes, u8, (N, k // 2)),
-        _arg(what, "a_scales", a_scales, u8, (N, k // 32)),
-        _arg(what, "counts", counts, torch.int32, (E,)),
-        _arg(what, "w_codes", w_codes, u8, wc), _arg(what, "w_scales", w_scales, u8, ws),
-        _arg(what, "w3_codes", w3_codes, u8, wc) if second else None,
-        _arg(what, "w3_scales", w3_scales, u8, ws) if second else None,
-        _arg(what, "out", out, _torch_dtype(dsc.out_dtype), (N, n)),
-        _arg(what, "workspace", workspace, u8, workspace.shape), workspace.numel(),
-        _stream(stream)), what)
+        dsc, _arg(what, "a_codes", a_codes, u8, (N, k // 2), dev),
+        _arg(what, "a_scales", a_scales, u8, (N, k // 32), dev),
+        _arg(what, "counts", counts, torch.int32, (E,), dev),
+        _arg(what, "w_codes", w_codes, u8, wc, dev), _arg(what, "w_scales", w_scales, u8, ws, dev),
+        _arg(what, "w3_codes", w3_codes, u8, wc, dev) if second else None,
+        _arg(what, "w3_scales", w3_scales, u8, ws, dev) if second else None,
+        _arg(what, "out", out, _torch_dtype(dsc.out_dtype), (N, n), dev), ws_at, ws_n,
+        _stream_on(stream, dev)), what)
 
 
 def mx4_check(dsc, workspace, stream=None):

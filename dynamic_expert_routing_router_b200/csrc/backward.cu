@@ -127,8 +127,11 @@ __global__ void __launch_bounds__(256) bw_token_kernel(const BwArgs a, const TIn
         const float sdot = s_sdot;
         if (a.renorm) {
             // Softmax over the candidates (Eq. 4): only they get a gradient.
-            for (int e = tid; e < E; e += blockDim.x)
-                a.dr[(long long)t * E + e] = s_gc[e] * (s_dg[e] - sdot);
+            for (int e = tid; e < E; e += blockDim.x) {
+                float v = s_gc[e] * (s_dg[e] - sdot);
+                if (a.dr_aux) v += a.dr_aux[(long long)t * E + e];
+                a.dr[(long long)t * E + e] = v;
+            }
         } else {
             // Softmax over all E logits: p_e for the others from the logits.
             const float *r = a.logits + (long long)t * 2 * E;
@@ -148,7 +151,9 @@ __global__ void __launch_bounds__(256) bw_token_kernel(const BwArgs a, const TIn
             for (int e = tid; e < E; e += blockDim.x) {
                 const bool is_c = s_gc[e] != 0.0f;
                 const float p = is_c ? s_gc[e] : expf(r[e] - rmax) / s_den;
-                a.dr[(long long)t * E + e] = p * (s_dg[e] - sdot);
+                float v = p * (s_dg[e] - sdot);
+                if (a.dr_aux) v += a.dr_aux[(long long)t * E + e];
+                a.dr[(long long)t * E + e] = v;
             }
         }
         __syncthreads();

@@ -863,8 +863,9 @@ beam_status make_bwd_plan(const beam_moe_desc *d, beam_moe_plan_info *P, BwdPlan
 
 beam_status backward_impl(const beam_moe_desc *d, const void *x, const void *Wg, const void *Wm,
                           const void *W1, const void *W3, const void *W2, const void *dy,
-                          float beta, float *dx, float *dWg, float *dWm, float *dW1, float *dW3,
-                          float *dW2, void *workspace, size_t ws_bytes, void *stream) {
+                          const float *dlogits, float beta, float *dx, float *dWg, float *dWm,
+                          float *dW1, float *dW3, float *dW2, void *workspace, size_t ws_bytes,
+                          void *stream) {
     beam_moe_plan_info P;
     BwdPlan B;
     beam_status s = make_bwd_plan(d, &P, &B);
@@ -872,6 +873,7 @@ beam_status backward_impl(const beam_moe_desc *d, const void *x, const void *Wg,
     if (!x || !Wg || !W1 || !W3 || !W2 || !dy || !dx || !dWg || !dW1 || !dW3 || !dW2)
         return BEAM_ERR_INVALID_ARG;
     if ((Wm == nullptr) != (dWm == nullptr) || !std::isfinite(beta)) return BEAM_ERR_INVALID_ARG;
+    if (!aligned16(dlogits)) return BEAM_ERR_INVALID_ARG;
     for (const void *p : {x, Wg, W1, W3, W2, dy, static_cast<const void *>(dx),
                           static_cast<const void *>(dWg), static_cast<const void *>(dW1),
                           static_cast<const void *>(dW3), static_cast<const void *>(dW2)})
@@ -1034,6 +1036,7 @@ beam_status backward_impl(const beam_moe_desc *d, const void *x, const void *Wg,
     a.u = reinterpret_cast<float *>(ws + B.off_u);
     a.dz = reinterpret_cast<float *>(ws + B.off_dz);
     a.dr = reinterpret_cast<float *>(ws + B.off_dr);
+    a.dr_aux = dlogits;
     a.dx = dx;
     BEAM_TRY_CUDA(launch_backward_stages(a, d->dtype, x, xp, dy, dyp, Wg, Wm, W1, W3, W2, dWg,
                                          dWm, dW1, dW3, dW2, n_sm, st, 0));
@@ -1137,8 +1140,18 @@ beam_status beam_moe_backward(const beam_moe_desc *desc, const void *x, const vo
                               const void *dy, float beta, float *dx, float *dW_gate,
                               float *dW_mask, float *dW1, float *dW3, float *dW2,
                               void *workspace, size_t workspace_bytes, void *stream) {
-    return backward_impl(desc, x, W_gate, W_mask, W1, W3, W2, dy, beta, dx, dW_gate, dW_mask,
-                         dW1, dW3, dW2, workspace, workspace_bytes, stream);
+    return backward_impl(desc, x, W_gate, W_mask, W1, W3, W2, dy, nullptr, beta, dx, dW_gate,
+                         dW_mask, dW1, dW3, dW2, workspace, workspace_bytes, stream);
+}
+
+beam_status beam_moe_backward_aux(const beam_moe_desc *desc, const void *x, const void *W_gate,
+                                  const void *W_mask, const void *W1, const void *W3,
+                                  const void *W2, const void *dy, const float *dlogits,
+                                  float beta, float *dx, float *dW_gate, float *dW_mask,
+                                  float *dW1, float *dW3, float *dW2, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    return backward_impl(desc, x, W_gate, W_mask, W1, W3, W2, dy, dlogits, beta, dx, dW_gate,
+                         dW_mask, dW1, dW3, dW2, workspace, workspace_bytes, stream);
 }
 
 int beam_moe_backward_kernel_count(const beam_moe_desc *desc) {

@@ -337,6 +337,7 @@ struct BwArgs {
     void *da_bf, *db_bf;     // [p_cap][I] bf16 copies of da, db (kept rows) or null
     float *u, *dz;           // [T][K]
     float *dr;               // [T][E]
+    const float *dr_aux;     // [T][E] added to dr, or null
     float *dx;               // [T][d]
 };
 // Each expert's candidate rows as tiles of at most rows_per_tile rows (one
@@ -369,6 +370,37 @@ struct Mx4Args {
     int *status;                // workspace: [0] CTAs, [64 + b] CTA b's DEV_* status
     unsigned long long timeout_ns;
     int fault_skip;             // tests: CTA 0 skips its first stage
+};
+
+// The residual block around the layer (block_norm.cu); null = left out.
+struct BlockArgs {
+    int T, d, accumulate;
+    float eps, res_scale, branch_scale;
+    const void *x;               // enter: the rows; exit: res; backward: out (or enter's rows)
+    const void *y, *w, *gc, *gt, *wn;
+    void *out, *n;
+    const void *dout;            // backward: of out (enter: of the skip path)
+    const float *dn;             // of n
+    void *dres, *dy;
+    float *dw, *dgc, *dgt, *dwn;
+    float *part;                 // [CTAs][2][d] column sums
+};
+
+// Balance loss (balance.cu).
+struct BalanceArgs {
+    int T, E, K, S, ld, has_mask, count_kept;
+    float thr, coef;
+    int C, chunks;               // tokens per chunk, chunks there can be
+    const float *logits;         // [T][ld]
+    const int *seq_begin;        // [S + 1] or null (one sequence)
+    float *loss, *prob;          // [1], [S][E]
+    int *cand, *kept;            // [S][E]
+    int *ticket;                 // sequences finished
+    float *part_p, *seq_loss;    // [chunks][E], [S]
+    int *part_c, *part_k;        // [chunks][E]
+    const int *counts;           // backward: [S][E]
+    const float *dloss;          // [1] or null (1)
+    float *dlogits;              // [T][E]
 };
 
 // fp32 SIMT path (BEAM_F32).

@@ -316,6 +316,15 @@ beam_status beam_moe_backward(const beam_moe_desc *desc, const void *x, const vo
                               const void *dy, float beta, float *dx, float *dW_gate,
                               float *dW_mask, float *dW1, float *dW3, float *dW2,
                               void *workspace, size_t workspace_bytes, void *stream);
+/* beam_moe_backward with a further gradient of the main router's logits,
+ * dlogits f32 [T,E] (beam_moe_balance_backward's), added to the layer's own
+ * before both go on to x and W_gate.  NULL: beam_moe_backward itself. */
+beam_status beam_moe_backward_aux(const beam_moe_desc *desc, const void *x, const void *W_gate,
+                                  const void *W_mask, const void *W1, const void *W3,
+                                  const void *W2, const void *dy, const float *dlogits,
+                                  float beta, float *dx, float *dW_gate, float *dW_mask,
+                                  float *dW1, float *dW3, float *dW2, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 /* Kernel launches of one beam_moe_backward call: 15 for bf16 (its dh = dy W2_e
  * product runs on the tensor cores, after a launch that lists each kept
  * expert's candidate rows), 14 for fp32; 0 for T = 0 or a bad descriptor. */
@@ -376,6 +385,111 @@ beam_status beam_moe_expert_rows(const beam_moe_desc *desc, const void *x_rows,
 beam_status beam_moe_ep_combine(const beam_moe_desc *desc, const float *y_rows,
                                 const int32_t *topk_idx, const float *topk_w,
                                 const int32_t *pair_pos, void *out, void *stream);
+
+/* ---------------------------------------------- the residual block around --
+ * What a transformer block puts around the layer, one pass over the rows
+ * each.  The pages leave the residual to the caller; these calls are that
+ * caller's part.  r(x) = 1 / sqrt(mean_j x_j^2 + eps) per row, in fp32.
+ *   T, d       token rows of width d; d % 8 == 0, d <= 16384
+ *   dtype      of the rows, the weights and the gates
+ *   eps        finite and > 0
+ *   res_scale, branch_scale   a and b below; finite
+ *   accumulate backward: 1 adds to the gradients of the weights and of
+ *              gate_c (fp32 [d]), 0 overwrites them; every other gradient is
+ *              overwritten
+ * Rows are contiguous, pointers 16-byte aligned.  An output may be the very
+ * buffer of one input row for row: n that of x, out that of res or y, n_next
+ * that of y or res (not out's), dres or dx that of dout or dskip, dy that of
+ * y.  Squares are summed in fp32: rows beyond 1e19 overflow.
+ * Rounding: one, to dtype, of each result; the next norm and the gradients
+ * read `out` as it is stored. */
+typedef struct {
+    int T, d;
+    int dtype; /* beam_dtype */
+    float eps, res_scale, branch_scale;
+    int accumulate; /* 0 or 1 */
+} beam_block_desc;
+
+/* n = x r(x) w: the rows the layer reads. */
+beam_status beam_block_enter(const beam_block_desc *desc, const void *x, const void *w, void *n,
+                             void *stream);
+
+/* out = a res + b s(gate_t[t]) gate_c[j] w_out[j] y r(y), with s the logistic
+ * function: the norm behind the layer, its gates and the residual;
+ * n_next = out r(out) w_next: the norm in front of the next block.
+ *   w_out [d] or NULL (y as it is, without r(y)), gate_c [d] or NULL (1),
+ *   gate_t [T] or NULL (s = 1), w_next [d] and n_next [T,d] or both NULL */
+beam_status beam_block_exit(const beam_block_desc *desc, const void *res, const void *y,
+                            const void *w_out, const void *gate_c, const void *gate_t, void *out,
+                            const void *w_next, void *n_next, void *stream);
+
+/* Bytes of workspace of the two backward calls (0 on a bad descriptor); it is
+ * 256-byte aligned, and calls that may overlap need one each. */
+size_t beam_block_workspace_size(const beam_block_desc *desc);
+
+/* dx = dskip + (dn through the norm), dw = sum_t dn x r(x).  dn fp32 [T,d],
+ * as beam_moe_backward writes its dx; dskip [T,d] of dtype or NULL: the
+ * gradient that reaches x past the block.  res_scale, branch_scale unused. */
+beam_status beam_block_enter_backward(const beam_block_desc *desc, const void *x, const void *w,
+                                      const float *dn, const void *dskip, void *dx, float *dw,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of beam_block_exit for dout [T,d] (dtype) and, with w_next,
+ * dn_next [T,d] (fp32): dres and dy [T,d] (dtype); dw_out, dgate_c, dw_next
+ * fp32 [d] and dgate_t fp32 [T], each given exactly when its weight or gate
+ * is.  y: as in the forward; out: the forward's, needed with w_next.  dy is
+ * the layer's upstream gradient (beam_moe_backward's dy).  Bitwise repeatable. */
+beam_status beam_block_exit_backward(const beam_block_desc *desc, const void *y, const void *out,
+                                     const void *w_out, const void *gate_c, const void *gate_t,
+                                     const void *w_next, const void *dout, const float *dn_next,
+                                     void *dres, void *dy, float *dw_out, float *dgate_c,
+                                     float *dgate_t, float *dw_next, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------- balance loss --
+ * The load-balance loss on the main router (news article on BEAM, §4: one of
+ * the three training losses; its form is not given, this is the usual one)
+ * over n_seq sequences of tokens, L_s long, with p_t the softmax of token t's
+ * logits over all E experts:
+ *   f_se = E / (K L_s) #{t in s with e among its K candidates}
+ *   P_se = 1 / L_s sum_{t in s} p_te
+ *   loss = coef / n_seq sum_s sum_e f_se P_se          (coef: even load)
+ * An empty sequence adds 0 and counts in n_seq.  Candidates are those of
+ * beam_moe_route: the K largest logits, ties to the lower id, NaN last.
+ * count_kept = 1 counts only the candidates the mask keeps (z >=
+ * mask_logit_threshold).  A row of -inf has no softmax and counts as zeros.
+ *   T tokens (< 2^30), n_seq <= 2^20, E <= 256, 1 <= K <= min(E, 16)
+ *   logits_ld  floats per row of logits: >= E, and >= 2E with has_mask, whose
+ *              columns [E, 2E) hold z -- beam_moe_route's logits have 2E */
+typedef struct {
+    int T, E, K, n_seq;
+    int logits_ld;
+    int has_mask, count_kept; /* 0 or 1 */
+    float mask_logit_threshold, coef;
+} beam_balance_desc;
+
+/* Forward.  logits f32 [T, logits_ld]; seq_begin int32 [n_seq + 1] (device) or
+ * NULL (n_seq == 1: all T): sequence s is tokens [seq_begin[s],
+ * seq_begin[s + 1]); tokens outside every sequence do not count.  Boundaries
+ * that decrease or leave [0, T] make the loss NaN.
+ * Written: loss f32 [1]; cand_counts int32 [n_seq, E]; kept_counts the same or
+ * NULL (only with has_mask); mean_prob f32 [n_seq, E] (P) or NULL.  Sums run
+ * in a fixed order.  Workspace 256-byte aligned; calls that may overlap need
+ * one each. */
+size_t beam_moe_balance_workspace_size(const beam_balance_desc *desc);
+beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
+                             const int32_t *seq_begin, float *loss, int32_t *cand_counts,
+                             int32_t *kept_counts, float *mean_prob, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* dlogits f32 [T,E] (overwritten): dloss coef / (n_seq L_s) p_te (f_se -
+ * sum_e' f_se' p_te'), zeros for tokens outside every sequence.  counts:
+ * cand_counts, or with count_kept kept_counts, of the forward (the counts pass
+ * no gradient); dloss f32 [1] (device) or NULL (1).  beam_moe_backward_aux
+ * carries dlogits on to x and W_gate. */
+beam_status beam_moe_balance_backward(const beam_balance_desc *desc, const float *logits,
+                                      const int32_t *seq_begin, const int32_t *counts,
+                                      const float *dloss, float *dlogits, void *stream);
 
 /* ------------------------------------- experts in 4-bit floating point --
  * The layer's experts with weights and token rows in MXFP4 (OCP Microscaling

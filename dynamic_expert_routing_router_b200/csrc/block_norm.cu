@@ -15,9 +15,12 @@
 //   S_j  = sum_t dz h:  dw = c S, dc = w S;  dw_next = sum_t dn o
 // enter's are g with x for out.
 //
-// Bound by memory: every element is read and written once, in 16-byte (fp32:
-// 32-byte) pieces that stay in registers between the sums and the results.
-// A group of warps owns a row; its sums are fp32 in a fixed order.
+// Bound by memory: every element is read from it and written to it once.  A
+// group of warps owns a row, a thread the same columns of all its group's
+// rows.  Each thread copies its columns of the next rows into shared memory
+// itself (cp.async, up to kMaxDepth rows ahead) and reads only its own copies,
+// so the loads need no barrier and no registers; a row is read from there as
+// often as its passes need it.  Sums are fp32 in a fixed order.
 #include <cuda_bf16.h>
 
 #include <initializer_list>
@@ -30,74 +33,145 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxD = 16384;
-constexpr int kMaxWarps = 16;  // of a CTA
+constexpr int kMaxDepth = 4;             // rows a thread loads ahead
+constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM for them
 
-// Eight consecutive elements, as stored.
+// Eight consecutive elements, as stored: one 16-byte piece of bf16, two of fp32.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
-    uint4 r;
-    __device__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
-    __device__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = r; }
-    __device__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ float get(int i) const {
-        const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
-        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    static constexpr int N = 1;
+    uint4 p[1];
+    __device__ float2 two(int i) const {  // elements 2 i and 2 i + 1
+        const uint32_t w = i == 0 ? p[0].x : i == 1 ? p[0].y : i == 2 ? p[0].z : p[0].w;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    __device__ void set(const float (&v)[8]) {  // one rounding, to the stored type
+    __device__ void set(const float2 (&v)[4]) {  // one rounding, to the stored type
         __nv_bfloat162 h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        r = *reinterpret_cast<uint4 *>(h);
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[i].x, v[i].y);
+        p[0] = *reinterpret_cast<uint4 *>(h);
     }
 };
 template <>
 struct Vec<float> {
-    float4 a, b;
-    __device__ void load(const float *p) {
-        a = *reinterpret_cast<const float4 *>(p);
-        b = *reinterpret_cast<const float4 *>(p + 4);
+    static constexpr int N = 2;
+    uint4 p[2];
+    __device__ float2 two(int i) const {
+        const uint4 &q = p[i >> 1];
+        return (i & 1) ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                       : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
     }
-    __device__ void store(float *p) const {
-        *reinterpret_cast<float4 *>(p) = a;
-        *reinterpret_cast<float4 *>(p + 4) = b;
-    }
-    __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ float get(int i) const {
-        const float4 &q = i < 4 ? a : b;
-        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    }
-    __device__ void set(const float (&v)[8]) {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
+    __device__ void set(const float2 (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            p[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y),
+                              __float_as_uint(v[2 * i + 1].x), __float_as_uint(v[2 * i + 1].y));
     }
 };
+template <typename T>
+__device__ __forceinline__ Vec<T> load_vec(const T *p) {
+    Vec<T> v;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) v.p[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T *p, const Vec<T> &v) {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) reinterpret_cast<uint4 *>(p)[i] = v.p[i];
+}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // v times eight consecutive weights.
 template <typename T>
-__device__ __forceinline__ void times(float (&v)[8], const T *w) {
-    Vec<T> q;
-    q.load(w);
+__device__ __forceinline__ void times(float2 (&v)[4], const T *w) {
+    const Vec<T> q = load_vec(w);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= q.get(k);
+    for (int k = 0; k < 4; ++k) v[k] = __fmul2_rn(v[k], q.two(k));
+}
+template <typename T>
+__device__ __forceinline__ void weights_of(float2 (&v)[4], const T *a, const T *b, int j) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = both(1.0f);
+    if (a) times(v, a + j);
+    if (b) times(v, b + j);
 }
 
+// ---------------------------------------------------------- loads ahead --
+// Shared memory of one group: [depth][planes][NV][lanes] 16-byte pieces, the
+// planes of a stage being those of the arrays it loads.
+struct Ring {
+    int depth, planes;
+    int at_x, at_y, at_g, at_n;  // first plane of each array; < 0: not loaded
+};
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Until at most `left` of the thread's copies (one group per row) are open.
+__device__ __forceinline__ void cp_async_wait(int left) {
+    if (left == 0)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (left == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void copy_ahead(uint4 *slot, int plane_step, const T *src) {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i)
+        cp_async16(slot + i * plane_step, reinterpret_cast<const uint4 *>(src) + i);
+}
+template <typename T>
+__device__ __forceinline__ Vec<T> read_copy(const uint4 *slot, int plane_step) {
+    Vec<T> v;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) v.p[i] = slot[i * plane_step];
+    return v;
+}
+
+// ------------------------------------------------------------- row sums --
 // A row's warps.  `slot` counts its reductions: two buffers in turn let one
 // barrier per reduction do (a buffer is written again only after every warp
 // has passed the next reduction's barrier, so after it has read this one).
 struct Row {
     int warps, group, lane, warp;  // warps per row, group in the CTA, lane, warp in the group
-    float *scratch;                // [2][groups][warps][N] of this CTA
+    float *scratch;                // this group's [2][warps][8]
     int slot;
 };
 
+__device__ __forceinline__ Row this_row(int warps, float *scratch) {
+    Row r;
+    r.warps = warps;
+    const int w = threadIdx.x >> 5;
+    r.group = w / warps;
+    r.warp = w - r.group * warps;
+    r.lane = threadIdx.x & 31;
+    r.scratch = scratch + r.group * warps * 16;
+    r.slot = 0;
+    return r;
+}
+
+__device__ __forceinline__ float *next_buffer(Row &r) {
+    float *s = r.scratch + (r.slot & 1) * r.warps * 8;
+    ++r.slot;
+    return s;
+}
 __device__ __forceinline__ void group_sync(const Row &r) {
-    if (r.warps > 1)
-        asm volatile("bar.sync %0, %1;" ::"r"(r.group + 1), "r"(r.warps * 32) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(r.group + 1), "r"(r.warps * 32) : "memory");
 }
 
 template <int N>
@@ -107,42 +181,55 @@ __device__ __forceinline__ void row_sum(Row &r, float (&v)[N]) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], o);
     if (r.warps == 1) return;
-    float *s = r.scratch + ((r.slot & 1) * kMaxWarps + r.group * r.warps) * N;
-    ++r.slot;
-    if (r.lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[r.warp * N + i] = v[i];
+    float *s = next_buffer(r);
+    if (r.lane < N) s[r.warp * 8 + r.lane] = r.lane == 0 ? v[0] : v[N - 1];
     group_sync(r);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float t = 0.0f;
-        for (int w = 0; w < r.warps; ++w) t += s[w * N + i];
-        v[i] = t;
-    }
+    for (int i = 0; i < N; ++i) v[i] = r.lane < r.warps ? s[r.lane * 8 + i] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], o);
 }
 
-__device__ __forceinline__ Row this_row(int warps, float *scratch) {
-    Row r;
-    r.warps = warps;
-    const int w = threadIdx.x >> 5;
-    r.group = w / warps;
-    r.warp = w - r.group * warps;
-    r.lane = threadIdx.x & 31;
-    r.scratch = scratch;
-    r.slot = 0;
-    return r;
+// Eight sums at once: each exchange halves the values a lane carries, nine
+// shuffles instead of forty.
+__device__ __forceinline__ void row_sum8(Row &r, float (&v)[8]) {
+#pragma unroll
+    for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+        const bool up = (r.lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n];
+            v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(kAll, send, o);
+        }
+    }
+    float t = v[0];  // of value lane / 4
+    t += __shfl_xor_sync(kAll, t, 2);
+    t += __shfl_xor_sync(kAll, t, 1);
+    if (r.warps > 1) {
+        float *s = next_buffer(r);
+        if ((r.lane & 3) == 0) s[r.warp * 8 + (r.lane >> 2)] = t;
+        group_sync(r);
+        t = 0.0f;
+        for (int w = r.lane >> 3; w < r.warps; w += 4) t += s[w * 8 + (r.lane & 7)];
+        t += __shfl_xor_sync(kAll, t, 8);
+        t += __shfl_xor_sync(kAll, t, 16);
+    }
+    const int step = r.warps > 1 ? 1 : 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kAll, t, i * step);
 }
 
 // ------------------------------------------------------------- forward --
-// The next row of a group is loaded before the current one's sums are waited
-// for, so the memory system never idles through a barrier.
-template <int NV>
-constexpr int kMinCtas = NV == 1 ? 2 : 1;
-
+// Weights stay in registers while a thread has one vector (NV = 1); the pair
+// w, gate_c is multiplied once.
 template <typename T, int NV, bool BRANCH>
-__global__ void __launch_bounds__(512, kMinCtas<NV>)
-    block_forward_kernel(const BlockArgs a, int warps) {
-    __shared__ float scratch[2 * kMaxWarps];
+__global__ void __launch_bounds__(1024, 1)
+    block_forward_kernel(const BlockArgs a, const Ring ring, int warps) {
+    constexpr bool KEEP = NV == 1;
+    extern __shared__ uint4 s_ring[];
+    __shared__ float scratch[2 * 32 * 8];
     griddep_wait();
     griddep_launch_dependents();
     Row row = this_row(warps, scratch);
@@ -155,75 +242,99 @@ __global__ void __launch_bounds__(512, kMinCtas<NV>)
     T *out = static_cast<T *>(a.out), *n = static_cast<T *>(a.n);
     const long long step = (long long)gridDim.x * groups;
     long long t = (long long)blockIdx.x * groups + row.group;
-    Vec<T> nx[NV], ny[NV];
-    auto fetch = [&](long long q) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (q < a.T && j < d) {
-                nx[i].load(x + q * d + j);
-                if (BRANCH) ny[i].load(y + q * d + j);
-            } else {
-                nx[i].zero();
-                if (BRANCH) ny[i].zero();
-            }
-        }
-    };
-    fetch(t);
-    for (; t < a.T; t += step) {
-        const long long at = t * d;
-        Vec<T> o[NV], v[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            o[i] = nx[i];
-            v[i] = ny[i];
-        }
-        fetch(t + step);
-        if (BRANCH) {
-            float s = a.branch_scale;
-            if (gt) s *= 1.0f / (1.0f + expf(-to_f(gt[t])));
-            if (w) {
-                float yy[1] = {0.0f};
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) yy[0] = fmaf(v[i].get(k), v[i].get(k), yy[0]);
-                row_sum(row, yy);
-                s *= rsqrtf(fmaf(yy[0], inv_d, a.eps));
-            }
+    const int plane = NV * lanes, stage_step = ring.planes * plane;
+    uint4 *base = s_ring + row.group * ring.depth * stage_step + me;
+    auto fetch = [&](long long q, int stage) {
+        if (q < a.T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int j = (i * lanes + me) * 8;
                 if (j >= d) continue;
-                float m[8], f[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m[k] = s;
-                if (w) times(m, w + j);
-                if (gc) times(m, gc + j);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = fmaf(a.res_scale, o[i].get(k), m[k] * v[i].get(k));
-                o[i].set(f);
-                o[i].store(out + at + j);
+                uint4 *s = base + stage * stage_step + i * lanes;
+                copy_ahead(s, plane, x + q * d + j);
+                if (BRANCH) copy_ahead(s + Vec<T>::N * plane, plane, y + q * d + j);
             }
         }
-        if (!wn) continue;
-        float sq[1] = {0.0f};
+        cp_async_commit();
+    };
+    for (int s = 0; s < ring.depth; ++s) fetch(t + s * step, s);
+    float2 mw[KEEP ? 4 : 1], nw[KEEP ? 4 : 1];
+    if constexpr (KEEP) {
+        const int j = me * 8 < d ? me * 8 : 0;
+        weights_of(mw, w, gc, j);
+        weights_of(nw, wn, static_cast<const T *>(nullptr), j);
+    }
+    float gate = gt && t < a.T ? to_f(gt[t]) : 0.0f;
+    for (int stage = 0; t < a.T; t += step) {
+        const long long at = t * d;
+        const float z = gate;
+        if (gt && t + step < a.T) gate = to_f(gt[t + step]);
+        cp_async_wait(ring.depth - 1);
+        const uint4 *src = base + stage * stage_step;
+        float s = a.branch_scale;
+        if (BRANCH) {
+            if (gt) s *= 1.0f / (1.0f + expf(-z));
+            if (w) {
+                float2 yy = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i) {
+                    if ((i * lanes + me) * 8 >= d) continue;
+                    const Vec<T> v = read_copy<T>(src + Vec<T>::N * plane + i * lanes, plane);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sq[0] = fmaf(o[i].get(k), o[i].get(k), sq[0]);
-        row_sum(row, sq);
-        const float r = rsqrtf(fmaf(sq[0], inv_d, a.eps));
+                    for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
+                }
+                float sum[1] = {yy.x + yy.y};
+                row_sum(row, sum);
+                s *= rsqrtf(fmaf(sum[0], inv_d, a.eps));
+            }
+        }
+        Vec<T> o[NV];
+        float2 oo = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * lanes + me) * 8;
             if (j >= d) continue;
-            float f[8];
+            o[i] = read_copy<T>(src + i * lanes, plane);
+            if (BRANCH) {
+                const Vec<T> v = read_copy<T>(src + Vec<T>::N * plane + i * lanes, plane);
+                float2 m[4], f[4];
+                if constexpr (KEEP) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] = o[i].get(k) * r;
-            times(f, wn + j);
+                    for (int k = 0; k < 4; ++k) m[k] = mw[k];
+                } else {
+                    weights_of(m, w, gc, j);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    f[k] = __ffma2_rn(both(a.res_scale), o[i].two(k),
+                                      __fmul2_rn(__fmul2_rn(m[k], both(s)), v.two(k)));
+                o[i].set(f);
+                store_vec(out + at + j, o[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) oo = __ffma2_rn(o[i].two(k), o[i].two(k), oo);
+        }
+        fetch(t + ring.depth * step, stage);
+        stage = stage + 1 == ring.depth ? 0 : stage + 1;
+        if (!wn) continue;
+        float sum[1] = {oo.x + oo.y};
+        row_sum(row, sum);
+        const float r = rsqrtf(fmaf(sum[0], inv_d, a.eps));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * lanes + me) * 8;
+            if (j >= d) continue;
+            float2 f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(o[i].two(k), both(r));
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(f[k], nw[k]);
+            } else {
+                times(f, wn + j);
+            }
             o[i].set(f);
-            o[i].store(n + at + j);
+            store_vec(n + at + j, o[i]);
         }
     }
 }
@@ -233,11 +344,14 @@ __global__ void __launch_bounds__(512, kMinCtas<NV>)
 // are summed before r(out) is known.  A thread owns its columns for all its
 // rows; a CTA's groups add theirs up in order, and each CTA writes one slab
 // [2][d] (S, dw_next) that block_columns_kernel adds up in order.
+constexpr int kBwThreads = 768;  // 80 registers a thread
+
 template <typename T, int NV, bool BRANCH>
-__global__ void __launch_bounds__(512, 1) block_backward_kernel(const BlockArgs a, int warps) {
-    constexpr bool AHEAD = NV * sizeof(T) <= 4;  // registers for the next row's loads
-    __shared__ float scratch[2 * kMaxWarps * 6];
-    extern __shared__ float s_cols[];  // [2][d]
+__global__ void __launch_bounds__(kBwThreads, 1)
+    block_backward_kernel(const BlockArgs a, const Ring ring, int warps) {
+    constexpr bool KEEP = NV == 1;
+    extern __shared__ uint4 s_ring[];
+    __shared__ float scratch[2 * 24 * 8];
     griddep_wait();
     griddep_launch_dependents();
     Row row = this_row(warps, scratch);
@@ -249,91 +363,122 @@ __global__ void __launch_bounds__(512, 1) block_backward_kernel(const BlockArgs 
     const T *gt = static_cast<const T *>(a.gt), *wn = static_cast<const T *>(a.wn);
     const T *dout = static_cast<const T *>(a.dout);
     T *dres = static_cast<T *>(a.dres), *dy = static_cast<T *>(a.dy);
-    float cs[NV][8], cn[NV][8];
+    float2 cs[NV][4], cn[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) cs[i][k] = cn[i][k] = 0.0f;
+        for (int k = 0; k < 4; ++k) cs[i][k] = cn[i][k] = both(0.0f);
     const long long step = (long long)gridDim.x * groups;
     long long t = (long long)blockIdx.x * groups + row.group;
-    struct Loads {
+    const int plane = NV * lanes, stage_step = ring.planes * plane;
+    uint4 *base = s_ring + row.group * ring.depth * stage_step + me;
+    auto fetch = [&](long long q, int stage) {
+        if (q < a.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int j = (i * lanes + me) * 8;
+                if (j >= d) continue;
+                uint4 *s = base + stage * stage_step + i * lanes;
+                const long long at = q * d + j;
+                if (ring.at_x >= 0) copy_ahead(s + ring.at_x * plane, plane, x + at);
+                if (ring.at_y >= 0) copy_ahead(s + ring.at_y * plane, plane, y + at);
+                if (ring.at_g >= 0) copy_ahead(s + ring.at_g * plane, plane, dout + at);
+                if (ring.at_n >= 0) copy_ahead(s + ring.at_n * plane, plane, a.dn + at);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < ring.depth; ++s) fetch(t + s * step, s);
+    float2 mw[KEEP ? 4 : 1], nw[KEEP ? 4 : 1];
+    if constexpr (KEEP) {
+        const int j = me * 8 < d ? me * 8 : 0;
+        weights_of(mw, w, gc, j);
+        weights_of(nw, wn, static_cast<const T *>(nullptr), j);
+    }
+    float gate = gt && t < a.T ? to_f(gt[t]) : 0.0f;
+    struct Pieces {
         Vec<T> o, y, g;
         Vec<float> n;
     };
-    Loads c[NV];
-    auto fetch = [&](Loads(&to)[NV], long long q) {
+    // Columns j of the row, of arrays that are not there zeros.
+    auto read = [&](Pieces &c, const uint4 *s, long long at) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            const bool in = q < a.T && j < d;
-            const long long at = q * d + j;
-            to[i].o.zero();
-            to[i].y.zero();
-            to[i].g.zero();
-            to[i].n.zero();
-            if (in && wn) {
-                to[i].o.load(x + at);
-                to[i].n.load(a.dn + at);
-            }
-            if (in && BRANCH) to[i].y.load(y + at);
-            if (in && dout) to[i].g.load(dout + at);
+        for (int i = 0; i < Vec<T>::N; ++i) c.o.p[i] = c.y.p[i] = c.g.p[i] = make_uint4(0u, 0u, 0u, 0u);
+        c.n.p[0] = c.n.p[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (wn) {
+            c.o = read_copy<T>(s + ring.at_x * plane, plane);
+            c.n = ring.at_n >= 0 ? read_copy<float>(s + ring.at_n * plane, plane)
+                                 : load_vec(a.dn + at);
         }
+        if (BRANCH) c.y = read_copy<T>(s + ring.at_y * plane, plane);
+        if (dout) c.g = read_copy<T>(s + ring.at_g * plane, plane);
     };
-    fetch(c, t);
-    for (; t < a.T; t += step) {
+    for (int stage = 0; t < a.T; t += step) {
         const long long at = t * d;
-        Loads ahead[AHEAD ? NV : 1];
-        if constexpr (AHEAD) fetch(ahead, t + step);
-        float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const float z = gate;
+        if (gt && t + step < a.T) gate = to_f(gt[t + step]);
+        cp_async_wait(ring.depth - 1);
+        const uint4 *src = base + stage * stage_step;
+        float2 q[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) q[k] = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int j = (i * lanes + me) * 8;
             if (j >= d) continue;
-            float m[8], p[8];
+            Pieces c;
+            read(c, src + i * lanes, at + j);
+            float2 m[4], p[4];
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                m[k] = c[i].y.get(k);
-                p[k] = c[i].n.get(k);
+                for (int k = 0; k < 4; ++k) {
+                    m[k] = mw[k];
+                    p[k] = nw[k];
+                }
+            } else {
+                weights_of(m, w, gc, j);
+                weights_of(p, wn, static_cast<const T *>(nullptr), j);
             }
-            if (BRANCH && w) times(m, w + j);
-            if (BRANCH && gc) times(m, gc + j);
-            if (wn) times(p, wn + j);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float o = c[i].o.get(k);
-                q[0] = fmaf(o, o, q[0]);
-                q[1] = fmaf(p[k], o, q[1]);
+            for (int k = 0; k < 4; ++k) {
+                const float2 o = c.o.two(k), pk = __fmul2_rn(p[k], c.n.two(k));
+                q[0] = __ffma2_rn(o, o, q[0]);
+                q[1] = __ffma2_rn(pk, o, q[1]);
                 if (BRANCH) {
-                    const float yk = c[i].y.get(k);
-                    q[2] = fmaf(yk, yk, q[2]);
-                    q[3] = fmaf(m[k], c[i].g.get(k), q[3]);
-                    q[4] = fmaf(m[k], p[k], q[4]);
-                    q[5] = fmaf(m[k], o, q[5]);
+                    const float2 yk = c.y.two(k), mk = __fmul2_rn(m[k], yk);
+                    q[2] = __ffma2_rn(yk, yk, q[2]);
+                    q[3] = __ffma2_rn(mk, c.g.two(k), q[3]);
+                    q[4] = __ffma2_rn(mk, pk, q[4]);
+                    q[5] = __ffma2_rn(mk, o, q[5]);
                 }
             }
         }
+        float sum[8];
         if (BRANCH) {
-            row_sum(row, q);
+#pragma unroll
+            for (int k = 0; k < 6; ++k) sum[k] = q[k].x + q[k].y;
+            sum[6] = sum[7] = 0.0f;
+            row_sum8(row, sum);
         } else {
-            float q2[2] = {q[0], q[1]};
-            row_sum(row, q2);
-            q[0] = q2[0];
-            q[1] = q2[1];
+            float two[2] = {q[0].x + q[0].y, q[1].x + q[1].y};
+            row_sum(row, two);
+            sum[0] = two[0];
+            sum[1] = two[1];
         }
-        const float ro = wn ? rsqrtf(fmaf(q[0], inv_d, a.eps)) : 0.0f;
+        const float ro = wn ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.0f;
         // mean(dn w o) of the formula, o normed; no power of r(out) above one
         // is formed, which tiny rows would take past fp32
-        const float mo = ro * q[1] * inv_d;
-        float sig = 1.0f, ry = 1.0f, dot = 0.0f, back = 0.0f;
+        const float mo = ro * sum[1] * inv_d;
+        float sig = 1.0f, ry = 1.0f, back = 0.0f;
         if (BRANCH) {
             float rest = 0.0f;  // 1 - sig, which near 1 has no digits left of sig's
             if (gt) {
-                const float z = to_f(gt[t]);
                 sig = 1.0f / (1.0f + expf(-z));
                 rest = 1.0f / (1.0f + expf(z));
             }
-            if (w) ry = rsqrtf(fmaf(q[2], inv_d, a.eps));
-            dot = a.branch_scale * sig * ry * (q[3] + ro * (q[4] - mo * (ro * q[5])));
+            if (w) ry = rsqrtf(fmaf(sum[2], inv_d, a.eps));
+            const float dot =
+                a.branch_scale * sig * ry * (sum[3] + ro * (sum[4] - mo * (ro * sum[5])));
             if (w) back = dot * inv_d;
             if (gt && me == 0) a.dgt[t] = rest * dot;
         }
@@ -342,144 +487,213 @@ __global__ void __launch_bounds__(512, 1) block_backward_kernel(const BlockArgs 
         for (int i = 0; i < NV; ++i) {
             const int j = (i * lanes + me) * 8;
             if (j >= d) continue;
-            float g[8], f[8];
+            Pieces c;
+            read(c, src + i * lanes, at + j);
+            float2 m[4], p[4], g[4], f[4];
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = c[i].n.get(k);
-            if (wn) times(g, wn + j);
+                for (int k = 0; k < 4; ++k) {
+                    m[k] = mw[k];
+                    p[k] = nw[k];
+                }
+            } else {
+                weights_of(m, w, gc, j);
+                weights_of(p, wn, static_cast<const T *>(nullptr), j);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float o = c[i].o.get(k) * ro;
-                g[k] = fmaf(ro, g[k] - mo * o, c[i].g.get(k));
-                cn[i][k] = fmaf(c[i].n.get(k), o, cn[i][k]);
-                f[k] = a.res_scale * g[k];
+            for (int k = 0; k < 4; ++k) {
+                const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
+                const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p[k], n));
+                g[k] = __ffma2_rn(both(ro), u, c.g.two(k));
+                cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
+                f[k] = __fmul2_rn(both(a.res_scale), g[k]);
             }
             Vec<T> r;
             r.set(f);
-            r.store(dres + at + j);
+            store_vec(dres + at + j, r);
             if constexpr (BRANCH) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    g[k] *= zs;  // dz
-                    cs[i][k] = fmaf(g[k], c[i].y.get(k) * ry, cs[i][k]);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 dz = __fmul2_rn(both(zs), g[k]);
+                    const float2 h = __fmul2_rn(c.y.two(k), both(ry));
+                    cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
+                    f[k] = __fmul2_rn(both(ry),
+                                      __ffma2_rn(dz, m[k], __fmul2_rn(h, both(-back))));
                 }
-                if (w) times(g, w + j);
-                if (gc) times(g, gc + j);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = ry * (g[k] - c[i].y.get(k) * ry * back);
                 r.set(f);
-                r.store(dy + at + j);
+                store_vec(dy + at + j, r);
             }
         }
-        if constexpr (AHEAD) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) c[i] = ahead[i];
-        } else {
-            fetch(c, t + step);
-        }
+        fetch(t + ring.depth * step, stage);
+        stage = stage + 1 == ring.depth ? 0 : stage + 1;
     }
     if (!a.part) return;
-    // The CTA's slab: its groups in order.
+    // The CTA's slab: its groups in order, in what was the ring.
+    cp_async_wait(0);
+    float *s_cols = reinterpret_cast<float *>(s_ring);  // [2][d]
     for (int g = 0; g < groups; ++g) {
-        if (row.group == g)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = (i * lanes + me) * 8;
-                if (j >= d) continue;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    s_cols[j + k] = g ? s_cols[j + k] + cs[i][k] : cs[i][k];
-                    s_cols[d + j + k] = g ? s_cols[d + j + k] + cn[i][k] : cn[i][k];
-                }
-            }
         __syncthreads();
+        if (row.group != g) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = (i * lanes + me) * 8;
+            if (j >= d) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float2 *s = reinterpret_cast<float2 *>(s_cols + j + 2 * k);
+                float2 *n = reinterpret_cast<float2 *>(s_cols + d + j + 2 * k);
+                *s = g ? __fadd2_rn(*s, cs[i][k]) : cs[i][k];
+                *n = g ? __fadd2_rn(*n, cn[i][k]) : cn[i][k];
+            }
+        }
     }
+    __syncthreads();
     float *slab = a.part + (long long)blockIdx.x * 2 * d;
-    for (int j = threadIdx.x * 4; j < 2 * d; j += blockDim.x * 4)
+    const int from = a.dw || a.dgc ? 0 : d, to = a.dwn ? 2 * d : d;
+    for (int j = from + threadIdx.x * 4; j < to; j += blockDim.x * 4)
         *reinterpret_cast<float4 *>(slab + j) = *reinterpret_cast<const float4 *>(s_cols + j);
 }
 
-// The slabs' sums, column by column in slab order (eight partial sums, then
-// those in order), and the weight gradients they give.
+// The slabs' sums and the weight gradients they give: 32 columns a CTA, thread
+// (p, c) adds four columns of slabs p, p + 32, ..., then the 32 parts are
+// added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) block_columns_kernel(const BlockArgs a, int slabs) {
-    __shared__ float s[2][8][32];
+    __shared__ float4 s[2][32][8];
     griddep_wait();
     griddep_launch_dependents();
-    const int c = threadIdx.x & 31, p = threadIdx.x >> 5, j = blockIdx.x * 32 + c;
-    float v0 = 0.0f, v1 = 0.0f;
-    if (j < a.d)
-        for (int b = p; b < slabs; b += 8) {
-            const float *q = a.part + (long long)b * 2 * a.d + j;
-            v0 += q[0];
-            v1 += q[a.d];
+    const int c = threadIdx.x & 7, p = threadIdx.x >> 3, j4 = (blockIdx.x * 8 + c) * 4;
+    const bool first = a.dw || a.dgc, second = a.dwn != nullptr;
+    float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (j4 < a.d) {
+#pragma unroll 4
+        for (int b = p; b < slabs; b += 32) {
+            const float *q = a.part + (long long)b * 2 * a.d + j4;
+            if (first) {
+                const float4 u = *reinterpret_cast<const float4 *>(q);
+                v[0].x += u.x; v[0].y += u.y; v[0].z += u.z; v[0].w += u.w;
+            }
+            if (second) {
+                const float4 u = *reinterpret_cast<const float4 *>(q + a.d);
+                v[1].x += u.x; v[1].y += u.y; v[1].z += u.z; v[1].w += u.w;
+            }
         }
-    s[0][p][c] = v0;
-    s[1][p][c] = v1;
-    __syncthreads();
-    if (p != 0 || j >= a.d) return;
-    v0 = v1 = 0.0f;
-    for (int b = 0; b < 8; ++b) {
-        v0 += s[0][b][c];
-        v1 += s[1][b][c];
     }
+    s[0][p][c] = v[0];
+    s[1][p][c] = v[1];
+    __syncthreads();
+    const int which = threadIdx.x >> 5, col = threadIdx.x & 31, j = blockIdx.x * 32 + col;
+    if (which > 1 || j >= a.d) return;
+    float t = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 32; ++b) t += reinterpret_cast<const float *>(&s[which][b][0])[col];
     const T *w = static_cast<const T *>(a.w), *gc = static_cast<const T *>(a.gc);
     auto put = [&](float *to, float v) { to[j] = a.accumulate ? to[j] + v : v; };
-    if (a.dw) put(a.dw, gc ? to_f(gc[j]) * v0 : v0);
-    if (a.dgc) put(a.dgc, w ? to_f(w[j]) * v0 : v0);
-    if (a.dwn) put(a.dwn, v1);
+    if (which == 0) {
+        if (a.dw) put(a.dw, gc ? to_f(gc[j]) * t : t);
+        if (a.dgc) put(a.dgc, w ? to_f(w[j]) * t : t);
+    } else if (a.dwn) {
+        put(a.dwn, t);
+    }
 }
 
 // --------------------------------------------------------------- launch --
-// Warps per row: a row's vectors of eight over its lanes, NV each.
+// Warps per row: a row's vectors of eight over its lanes, nv each.
 struct Shape {
-    int nv, warps, groups, grid;
+    int nv, warps, groups, grid, per_sm;
 };
 
 Shape shape_of(const beam_block_desc *d, bool backward) {
     Shape s;
-    const int vecs = d->d / 8;
-    s.nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    const int vecs = d->d / 8, most = backward ? kBwThreads : 1024;
+    s.nv = (vecs + most - 1) / most;
     s.warps = (vecs + 32 * s.nv - 1) / (32 * s.nv);
-    s.groups = kMaxWarps / s.warps;
-    if (s.groups > 15) s.groups = 15;  // named barriers 1..15
+    // Backward: one CTA per SM, so that there are few slabs.  Forward: CTAs of
+    // at least four warps, several per SM.  Named barriers are 1..15.
+    s.groups = backward ? most / 32 / s.warps : s.warps < 4 ? 4 / s.warps : 1;
+    if (s.groups > 15) s.groups = 15;
     // rather a row on every SM than several on a few
     const int rows = d->T / kNominalSMs;
     if (s.groups > rows) s.groups = rows > 1 ? rows : 1;
-    const long long want = ((long long)d->T + s.groups - 1) / s.groups;
     const int threads = s.groups * s.warps * 32;
-    const int per_sm = backward || s.nv > 1 ? 512 / threads : 1024 / threads;
-    const long long cap = (long long)kNominalSMs * per_sm;
+    s.per_sm = backward ? 1 : 1024 / threads < 8 ? 1024 / threads : 8;
+    const long long want = ((long long)d->T + s.groups - 1) / s.groups;
+    const long long cap = (long long)kNominalSMs * s.per_sm;
     s.grid = int(want < cap ? want : cap);
     return s;
+}
+
+// Planes: 16-byte pieces per eight elements of one stage.
+Ring ring_of(const BlockArgs &a, int elt, bool branch, bool backward) {
+    Ring r = {0, 0, -1, -1, -1, -1};
+    const int n = elt / 2;
+    auto add = [&](int &at, int pieces) {
+        at = r.planes;
+        r.planes += pieces;
+    };
+    if (!backward || a.wn) add(r.at_x, n);
+    if (branch) add(r.at_y, n);
+    if (backward && a.dout) add(r.at_g, n);
+    if (backward && a.wn) add(r.at_n, 2);
+    return r;
+}
+
+// Rows ahead: as many as shared memory holds, and no more than there are.
+// The widest fp32 rows leave no room for dn, which is then read in place.
+size_t ring_fit(Ring &r, const Shape &s, int T) {
+    const size_t piece = size_t(s.groups) * s.warps * 32 * s.nv * 16;
+    const size_t room = size_t(kRingBytes) / s.per_sm;
+    if (r.at_n >= 0 && r.planes * piece > room) {
+        r.at_n = -1;
+        r.planes -= 2;
+    }
+    const size_t stage = r.planes * piece;
+    const long long rows = ((long long)T + s.grid * (long long)s.groups - 1) / (s.grid * (long long)s.groups);
+    r.depth = kMaxDepth;
+    while (r.depth > 1 && (r.depth * stage > room || r.depth > rows)) --r.depth;
+    return r.depth * stage;
 }
 
 size_t slab_bytes(const beam_block_desc *d) {
     return d->T == 0 ? 0 : size_t(shape_of(d, true).grid) * 2 * size_t(d->d) * sizeof(float);
 }
 
+constexpr int kSmemMost = 208 * 1024;
+
+template <typename T, int NV, bool BRANCH>
+cudaError_t launch_forward_nv(const BlockArgs &a, const Shape &s, cudaStream_t st) {
+    auto kern = block_forward_kernel<T, NV, BRANCH>;
+    static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
+    cudaError_t e = set_smem_once(kern, kSmemMost, attr_set);
+    if (e != cudaSuccess) return e;
+    Ring r = ring_of(a, sizeof(T), BRANCH, false);
+    const size_t smem = ring_fit(r, s, a.T);
+    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, r, s.warps);
+}
+
 template <typename T, bool BRANCH>
 cudaError_t launch_forward(const BlockArgs &a, const Shape &s, cudaStream_t st) {
-    const dim3 grid(s.grid), block(s.groups * s.warps * 32);
-    if (s.nv == 1) return launch_pdl(block_forward_kernel<T, 1, BRANCH>, grid, block, 0, st, a, s.warps);
-    if (s.nv == 2) return launch_pdl(block_forward_kernel<T, 2, BRANCH>, grid, block, 0, st, a, s.warps);
-    return launch_pdl(block_forward_kernel<T, 4, BRANCH>, grid, block, 0, st, a, s.warps);
+    return s.nv == 1 ? launch_forward_nv<T, 1, BRANCH>(a, s, st)
+                     : launch_forward_nv<T, 2, BRANCH>(a, s, st);
 }
 
 template <typename T, int NV, bool BRANCH>
-cudaError_t launch_backward_nv(const BlockArgs &a, const Shape &s, cudaStream_t st) {
+cudaError_t launch_backward_nv(const BlockArgs &a, Shape s, cudaStream_t st) {
     auto kern = block_backward_kernel<T, NV, BRANCH>;
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
-    cudaError_t e = set_smem_once(kern, kMaxD * 8, attr_set);
+    cudaError_t e = set_smem_once(kern, kSmemMost, attr_set);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32),
-                      a.part ? size_t(a.d) * 8 : 0, st, a, s.warps);
+    Ring r = ring_of(a, sizeof(T), BRANCH, true);
+    size_t smem = ring_fit(r, s, a.T);
+    if (a.part && smem < size_t(a.d) * 8) smem = size_t(a.d) * 8;
+    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, r, s.warps);
 }
 
 template <typename T, bool BRANCH>
 cudaError_t launch_backward(const BlockArgs &a, const Shape &s, cudaStream_t st) {
     cudaError_t e = s.nv == 1   ? launch_backward_nv<T, 1, BRANCH>(a, s, st)
                     : s.nv == 2 ? launch_backward_nv<T, 2, BRANCH>(a, s, st)
-                                : launch_backward_nv<T, 4, BRANCH>(a, s, st);
+                                : launch_backward_nv<T, 3, BRANCH>(a, s, st);
     if (e != cudaSuccess || !a.part) return e;
     return launch_pdl(block_columns_kernel<T>, dim3((a.d + 31) / 32), dim3(256), 0, st, a, s.grid);
 }

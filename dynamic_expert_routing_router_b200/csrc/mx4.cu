@@ -6,6 +6,7 @@
 // value is v / 2^X rounded to nearest-even on the grid +-{0, .5, 1, 1.5, 2, 3,
 // 4, 6} (E2M1), larger magnitudes saturating at 6.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "beam_internal.h"
 #include "beam_ptx.cuh"
@@ -16,23 +17,49 @@ namespace {
 // ------------------------------------------------------------- quantise --
 // Four lanes share a block of 32 values, eight each: a warp reads 512
 // contiguous bytes of bf16 per load and writes 128 of codes.  Scaling by 2^-X
-// is exact, so each value is rounded once, by the conversion.
+// is exact, so each value is rounded once, by the conversion.  Bound by
+// memory: kMxAhead loads of a thread are under way at a time.
 
-__device__ __forceinline__ void load_eight(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+constexpr int kMxAhead = 4;
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 r;
+    __device__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
+    __device__ float2 two(int i) const {
+        const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-}
-__device__ __forceinline__ void load_eight(const float *p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+    // The largest magnitude's bits as those of a float; NaN above infinity.
+    __device__ uint32_t top() const {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(r.x & kAbs, r.y & kAbs), __vmaxu2(r.z & kAbs, r.w & kAbs));
+        return max(m >> 16, m & 0xffffu) << 16;
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ float2 two(int i) const {
+        const float4 &q = i < 2 ? a : b;
+        return (i & 1) ? make_float2(q.z, q.w) : make_float2(q.x, q.y);
+    }
+    __device__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = two(i);
+            m = max(m, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu));
+        }
+        return m;
+    }
+};
 
 // Two values to E2M1 (round to nearest even, saturating): lo in bits 0-3.
 __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
@@ -67,42 +94,52 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, long long
     const long long total = rows * (cols >> 3);  // eights; a block's four never split
     const int blocks = cols >> 5;
     const long long step = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        float v[8];
-        load_eight(x + i * 8, v);
-        uint32_t m = 0;
+    const unsigned quad = 0xfu << (threadIdx.x & 28);
+    for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total;
+         i0 += kMxAhead * step) {
+        Eight<T> v[kMxAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-        const unsigned quad = 0xfu << (threadIdx.x & 28);
-        m = max(m, __shfl_xor_sync(quad, m, 1));
-        m = max(m, __shfl_xor_sync(quad, m, 2));
-        const int field = int(m >> 23);  // exponent + 127 of the largest; 0: subnormal or zero
-        const bool bad = field == 255;   // infinity or NaN: the whole block stands for NaN
-        const int s = field > 2 ? field - 2 : 0;
-        const float inv = __uint_as_float(uint32_t(254 - s) << 23);  // 2^-X
-        uint32_t out = 0;
+        for (int q = 0; q < kMxAhead; ++q)
+            if (i0 + q * step < total) v[q].load(x + (i0 + q * step) * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            out |= to_e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-        codes[i] = bad ? 0u : out;
-        if ((threadIdx.x & 3) == 0) {
-            const long long b = i >> 2;
-            long long at = b;
-            if (tiled) at = tiled_at(b / blocks, int(b % blocks), blocks);
-            scales[at] = bad ? 255 : uint8_t(s);
+        for (int q = 0; q < kMxAhead; ++q) {
+            const long long i = i0 + q * step;
+            if (i >= total) break;
+            uint32_t m = v[q].top();
+            m = max(m, __shfl_xor_sync(quad, m, 1));
+            m = max(m, __shfl_xor_sync(quad, m, 2));
+            const int field = int(m >> 23);  // exponent + 127 of the largest; 0: subnormal or zero
+            const bool bad = field == 255;   // infinity or NaN: the whole block stands for NaN
+            const int s = field > 2 ? field - 2 : 0;
+            const float inv = __uint_as_float(uint32_t(254 - s) << 23);  // 2^-X
+            uint32_t out = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = __fmul2_rn(v[q].two(j), make_float2(inv, inv));
+                out |= to_e2m1x2(u.x, u.y) << (8 * j);
+            }
+            codes[i] = bad ? 0u : out;
+            if ((threadIdx.x & 3) == 0) {
+                const long long b = i >> 2;
+                long long at = b;
+                if (tiled) at = tiled_at(b / blocks, int(b % blocks), blocks);
+                scales[at] = bad ? 255 : uint8_t(s);
+            }
         }
     }
 }
 
 // ----------------------------------------------------------- read back --
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    // 3-bit magnitude as bits of a float with exponent field 126 + ..: the
-    // subnormal code 1 is 0.5, codes 2..7 are (1 + m/2) 2^(e-1).
-    const uint32_t a = c & 7u;
-    const float v = a < 2u ? 0.5f * float(a)
-                           : __uint_as_float(((a >> 1) + 126u) << 23 | (a & 1u) << 22);
-    return (c & 8u) ? -v : v;
+// Two E2M1 values (bits 0-3 and 4-7) as floats; a half holds each exactly.
+__device__ __forceinline__ float2 from_e2m1x2(uint32_t c) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.u8.u32 b, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+        : "=r"(h)
+        : "r"(c));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 __device__ __forceinline__ void store_eight(__nv_bfloat16 *p, const float (&v)[8]) {
@@ -126,17 +163,33 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *cod
     const long long total = rows * (cols >> 3);
     const int blocks = cols >> 5;
     const long long step = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const uint32_t c = codes[i];
-        const long long b = i >> 2;
-        const uint32_t s = scales[tiled ? tiled_at(b / blocks, int(b % blocks), blocks) : b];
-        // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
-        const float f = s == 0 ? __uint_as_float(0x00400000u)
-                               : __uint_as_float(s == 255u ? 0x7fc00000u : s << 23);
-        float v[8];
+    for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total;
+         i0 += kMxAhead * step) {
+        uint32_t c[kMxAhead], s[kMxAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * f;
-        store_eight(out + i * 8, v);
+        for (int q = 0; q < kMxAhead; ++q) {
+            const long long i = i0 + q * step;
+            if (i >= total) break;
+            c[q] = codes[i];
+            const long long b = i >> 2;
+            s[q] = scales[tiled ? tiled_at(b / blocks, int(b % blocks), blocks) : b];
+        }
+#pragma unroll
+        for (int q = 0; q < kMxAhead; ++q) {
+            const long long i = i0 + q * step;
+            if (i >= total) break;
+            // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
+            const float f = s[q] == 0 ? __uint_as_float(0x00400000u)
+                                      : __uint_as_float(s[q] == 255u ? 0x7fc00000u : s[q] << 23);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = __fmul2_rn(from_e2m1x2(c[q] >> (8 * j)), make_float2(f, f));
+                v[2 * j] = u.x;
+                v[2 * j + 1] = u.y;
+            }
+            store_eight(out + i * 8, v);
+        }
     }
 }
 

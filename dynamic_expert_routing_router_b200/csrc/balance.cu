@@ -9,10 +9,15 @@
 // (1 per sequence where the load is even), and since f only counts,
 //   dr_te = dloss coef / (S L_s) p_te (f_se - sum_e' f_se' p_te').
 //
-// Forward: a CTA takes a chunk of one sequence, a warp a token at a time, lane
-// l experts l, l + 32, ...; its probabilities and counts stay in registers
-// over its tokens and are added up over the CTA's warps and the chunks in a
-// fixed order, so the loss is bitwise repeatable.
+// Forward: CTA v takes the tokens [v C, (v + 1) C) and adds up, per sequence
+// that begins, ends or runs there, its probabilities and counts: part v + s of
+// sequence s (one part per chunk or sequence begun, so no two share an index).
+// A warp takes a token at a time, lane l experts l, l + 32, ..., the next
+// token's logits being loaded meanwhile; a second launch adds the parts up.
+// Every sum runs in a fixed order: the loss is bitwise repeatable.
+//
+// Bound by instructions: about 40 per 32 logits for the K largest, the softmax
+// and the sums, against one 128-byte load.
 #include "beam_internal.h"
 #include "beam_ptx.cuh"
 
@@ -21,6 +26,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBalWarps = 8;
+constexpr int kMaxChunk = 1 << 18;  // tokens: a warp's counts fit 16 bits
 
 // Sequence boundaries as given, made safe: inside [0, T] and not decreasing.
 struct Span {
@@ -36,292 +42,330 @@ __device__ __forceinline__ Span span_of(const BalanceArgs &a, int s) {
     return r;
 }
 
-// Which sequence and chunk of it the v-th chunk of the batch is: sequences
-// have ceil(L / C) chunks each.  One warp; false if there are fewer chunks.
-// *first: the index of the sequence's first chunk.
-__device__ __forceinline__ bool find_chunk(const BalanceArgs &a, int v, int *seq, int *first) {
+// The first sequence that ends behind token t (S if none does), by one warp:
+// each step leaves one of 32 parts of the boundaries.
+__device__ __forceinline__ int first_ending_after(const BalanceArgs &a, int t) {
+    if (!a.seq_begin) return t < a.T ? 0 : 1;
     const int lane = threadIdx.x & 31;
-    int base = 0;
-    for (int s0 = 0; s0 < a.S; s0 += 32) {
-        int c = 0;
-        if (s0 + lane < a.S) {
-            const Span sp = span_of(a, s0 + lane);
-            c = (sp.hi - sp.lo + a.C - 1) / a.C;
-        }
-        int sum = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kAll, sum, o);
-            if (lane >= o) sum += u;
-        }
-        const unsigned past = __ballot_sync(kAll, base + sum > v);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            *seq = s0 + l;
-            *first = base + __shfl_sync(kAll, sum - c, l);
-            return true;
-        }
-        base += __shfl_sync(kAll, sum, 31);
+    int lo = 0, hi = a.S;  // it is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const unsigned past = __ballot_sync(kAll, at >= hi || a.seq_begin[at + 1] > t);
+        if (!past) return hi;  // not even the last one
+        const int l = __ffs(past) - 1;
+        hi = min(hi, lo + (l + 1) * step - 1);
+        lo += l * step;
     }
-    return false;
+    return lo;
 }
 
-// Larger logit -> larger key; -0 counts as +0, NaN as -infinity; 0 is taken.
-__device__ __forceinline__ unsigned key_of(float r) {
-    const float v = r == 0.0f ? 0.0f : (r != r) ? -INFINITY : r;
-    const unsigned b = __float_as_uint(v);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
-
-template <int EPL>
-__device__ __forceinline__ float row_max(const float (&r)[EPL]) {
-    float m = -INFINITY;
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, r[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    return m;
-}
-
-// r becomes the softmax of the row.  A row of -infinities has none: zeros.
-template <int EPL>
-__device__ __forceinline__ void softmax_row(float (&r)[EPL], int E) {
-    const int lane = threadIdx.x & 31;
-    const float m = row_max(r);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        // NaN logits reach the sum as NaN; fmaxf leaves them out of m
-        r[i] = lane + 32 * i < E ? (r[i] == -INFINITY ? 0.0f : expf(r[i] - m)) : 0.0f;
-        sum += r[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) r[i] *= inv;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
 }
 
 template <int EPL>
 __device__ __forceinline__ void load_row(const float *p, int E, float (&r)[EPL]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) r[i] = lane + 32 * i < E ? p[lane + 32 * i] : -INFINITY;
+    for (int i = 0; i < EPL; ++i) r[i] = lane + 32 * i < E ? __ldcs(p + lane + 32 * i) : -INFINITY;
+}
+
+// r, whose largest value (NaN left out) is m, becomes the softmax of the row.
+// A row of -infinities has none: zeros.  NaN logits reach the sum as NaN.
+template <int EPL>
+__device__ __forceinline__ void softmax_row(float (&r)[EPL], float m) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        r[i] = r[i] == -INFINITY ? 0.0f : expf(r[i] - m);
+        sum += r[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) r[i] *= inv;
+}
+
+// Bit i: expert lane + 32 i is among the K largest of the row (ties to the
+// lower id, NaN as -infinity); *m the largest.  Each lane sorts its values;
+// then the largest heads are taken off, all that are equal at once, until K
+// are: the last one is the K-th largest.
+template <int EPL>
+__device__ __forceinline__ unsigned largest(const float (&r)[EPL], int E, int K, float *m) {
+    const int lane = threadIdx.x & 31;
+    float h[EPL], v[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) h[i] = v[i] = fmaxf(r[i], -INFINITY);
+    // odd-even merge sort, descending
+#pragma unroll
+    for (int p = 1; p < EPL; p <<= 1)
+#pragma unroll
+        for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < EPL; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < EPL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const float x = h[i + j], y = h[i + j + k];
+                        h[i + j] = fmaxf(x, y);
+                        h[i + j + k] = fminf(x, y);
+                    }
+    float kth = 0.0f;
+    int got = 0;
+    for (int k = 0; k < K && got < K; ++k) {
+        kth = warp_max(h[0]);
+        if (k == 0) *m = kth;
+        const bool mine = h[0] == kth;
+        got += __popc(__ballot_sync(kAll, mine));
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; ++i) h[i] = h[i + 1];
+            h[EPL - 1] = -INFINITY;
+        }
+    }
+    unsigned taken = 0;
+    // Exactly K values reach the K-th: they are the ones.  (Equal heads of one
+    // lane come off one by one, so look whether one more is left.)
+    if (got == K && kth != -INFINITY && !__any_sync(kAll, h[0] == kth)) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) taken |= v[i] >= kth ? 1u << i : 0u;
+        return taken;
+    }
+    // Ties: those above, then the lowest ids of the equal ones.
+    int more = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) more += __popc(__ballot_sync(kAll, v[i] > kth));
+    int left = K - more;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const bool tie = lane + 32 * i < E && v[i] == kth;
+        const unsigned b = __ballot_sync(kAll, tie);
+        const int before = __popc(b & ((1u << lane) - 1u));
+        if (v[i] > kth || (tie && before < left)) taken |= 1u << i;
+        left -= min(left, __popc(b));
+    }
+    return taken;
 }
 
 template <int EPL>
-__global__ void __launch_bounds__(kBalWarps * 32) balance_chunk_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
+    balance_chunk_kernel(const BalanceArgs a) {
     __shared__ float s_p[kBalWarps][32 * EPL];
-    __shared__ int s_c[kMaxE], s_k[kMaxE];
+    __shared__ unsigned s_c[kBalWarps][32 * EPL];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-    int seq, first;
-    if (!find_chunk(a, blockIdx.x, &seq, &first)) return;  // the same in every warp
-    const Span sp = span_of(a, seq);
-    const int t0 = sp.lo + (int(blockIdx.x) - first) * a.C, t1 = min(sp.hi, t0 + a.C);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) s_c[e] = s_k[e] = 0;
-    __syncthreads();
-    float acc[EPL];
-    int cand[EPL], kept[EPL];
+    const int t0 = blockIdx.x * a.C, t1 = min(a.T, t0 + a.C);
+    const bool mask = a.has_mask && (a.kept || a.count_kept);
+    for (int s = first_ending_after(a, t0); s < a.S; ++s) {
+        const Span sp = span_of(a, s);
+        if (sp.lo >= t1 && !sp.bad) break;
+        const int lo = max(sp.lo, t0), hi = min(sp.hi, t1);
+        if (lo >= hi) continue;
+        float acc[EPL];
+        unsigned count[EPL];  // candidates, and above bit 16 kept ones
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        acc[i] = 0.0f;
-        cand[i] = kept[i] = 0;
-    }
-    for (int t = t0 + warp; t < t1; t += kBalWarps) {
-        const float *row = a.logits + (long long)t * a.ld;
-        float r[EPL];
-        load_row(row, E, r);
-        unsigned key[EPL], taken = 0;
+        for (int i = 0; i < EPL; ++i) {
+            acc[i] = 0.0f;
+            count[i] = 0u;
+        }
+        float next[EPL], znext[EPL];
+        auto load = [&](int t) {
+            const float *row = a.logits + (long long)t * a.ld;
+            load_row(row, E, next);
+            if (mask) load_row(row + E, E, znext);
+        };
+        int t = lo + warp;
+        if (t < hi) load(t);
+        for (; t < hi; t += kBalWarps) {
+            float r[EPL], z[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = lane + 32 * i < E ? key_of(r[i]) : 0u;
-        for (int k = 0; k < a.K; ++k) {
-            unsigned best = 0u;
-            int at = 0;
+            for (int i = 0; i < EPL; ++i) {
+                r[i] = next[i];
+                z[i] = znext[i];
+            }
+            if (t + kBalWarps < hi) load(t + kBalWarps);
+            float m;
+            const unsigned taken = largest(r, E, a.K, &m);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
-            const unsigned top = __reduce_max_sync(kAll, best);
-            // of the lanes that hold it, the lowest expert
-            const unsigned id =
-                __reduce_min_sync(kAll, best == top ? unsigned(lane + 32 * at) : ~0u);
-            if (id == unsigned(lane + 32 * at)) {
-                taken |= 1u << at;
+                if ((taken >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
+            softmax_row(r, m);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (i == at) key[i] = 0u;
-            }
+            for (int i = 0; i < EPL; ++i) acc[i] += r[i];
         }
+        __syncthreads();  // the previous sequence's sums are out
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if ((taken >> i) & 1u) {
-                ++cand[i];
-                if (a.has_mask && row[E + lane + 32 * i] >= a.thr) ++kept[i];
+        for (int i = 0; i < EPL; ++i) {
+            s_p[warp][lane + 32 * i] = acc[i];
+            s_c[warp][lane + 32 * i] = count[i];
+        }
+        __syncthreads();
+        const long long at = ((long long)blockIdx.x + s) * E;
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            float v = 0.0f;
+            int c = 0, k = 0;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) {
+                v += s_p[w][e];
+                c += s_c[w][e] & 0xffffu;
+                k += s_c[w][e] >> 16;
             }
-        softmax_row(r, E);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) acc[i] += r[i];
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        s_p[warp][e] = acc[i];
-        if (cand[i]) atomicAdd(&s_c[e], cand[i]);
-        if (kept[i]) atomicAdd(&s_k[e], kept[i]);
-    }
-    __syncthreads();
-    const long long at = (long long)blockIdx.x * E;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kBalWarps; ++w) v += s_p[w][e];
-        a.part_p[at + e] = v;
-        a.part_c[at + e] = s_c[e];
-        a.part_k[at + e] = s_k[e];
+            a.part_p[at + e] = v;
+            a.part_c[at + e] = c;
+            if (mask) a.part_k[at + e] = k;
+        }
     }
 }
 
-// One CTA per sequence: its chunks in order, its counts, probabilities and
-// loss; the last CTA to finish adds the sequences' losses up in order.
-__global__ void __launch_bounds__(256) balance_final_kernel(const BalanceArgs a) {
-    __shared__ float s_sum[8];
-    __shared__ int s_last, s_first;
+// CTA (s, j): sequence s, experts [32 j, 32 j + 32); warp w adds up parts w, w
+// + warps, ..., then warp 0 the warps' sums in order.  The last CTA to finish
+// adds the losses of all in order.
+__global__ void __launch_bounds__(1024) balance_final_kernel(const BalanceArgs a) {
+    __shared__ float s_p[32][32];
+    __shared__ int s_c[32][32], s_k[32][32];
+    __shared__ int s_last;
     griddep_wait();
     griddep_launch_dependents();
-    const int s = blockIdx.x, e = threadIdx.x;
-    const int lane = e & 31, warp = e >> 5;
+    const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = blockDim.x >> 5, e = blockIdx.y * 32 + lane;
     const Span sp = span_of(a, s);
-    const int L = sp.hi - sp.lo, chunks = (L + a.C - 1) / a.C;
-    if (warp == 0) {  // chunks before this sequence's
-        int n = 0;
-        for (int q = lane; q < s; q += 32) {
-            const Span o = span_of(a, q);
-            n += (o.hi - o.lo + a.C - 1) / a.C;
-        }
-        n = int(__reduce_add_sync(kAll, unsigned(n)));
-        if (lane == 0) s_first = n;
-    }
-    __syncthreads();
-    float term = 0.0f;
-    if (e < a.E) {
-        float p = 0.0f;
-        int c = 0, k = 0;
-        for (int q = 0; q < chunks && s_first + q < a.chunks; ++q) {
-            const long long at = (long long)(s_first + q) * a.E + e;
+    const bool mask = a.has_mask && (a.kept || a.count_kept);
+    float p = 0.0f;
+    int c = 0, k = 0;
+    if (e < a.E && sp.hi > sp.lo) {
+        const int last = (sp.hi - 1) / a.C;
+#pragma unroll 4
+        for (int v = sp.lo / a.C + warp; v <= last; v += warps) {
+            const long long at = ((long long)v + s) * a.E + e;
             p += a.part_p[at];
             c += a.part_c[at];
-            k += a.part_k[at];
+            if (mask) k += a.part_k[at];
         }
-        const float len = float(L > 0 ? L : 1);
-        const long long o = (long long)s * a.E + e;
-        a.cand[o] = c;
-        if (a.kept) a.kept[o] = k;
-        if (a.prob) a.prob[o] = p / len;
-        term = float(a.count_kept ? k : c) * float(a.E) / (float(a.K) * len) * (p / len);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(kAll, term, o);
-    if (lane == 0) s_sum[warp] = term;
+    s_p[warp][lane] = p;
+    s_c[warp][lane] = c;
+    s_k[warp][lane] = k;
     __syncthreads();
-    if (e == 0) {
-        float v = 0.0f;
-        for (int w = 0; w < 8; ++w) v += s_sum[w];
-        a.seq_loss[s] = sp.bad ? NAN : v;
-        __threadfence();
-        s_last = atomicAdd(a.ticket, 1) == a.S - 1;
+    if (warp == 0) {
+        float term = 0.0f;
+        if (e < a.E) {
+            for (int w = 1; w < warps; ++w) {
+                p += s_p[w][lane];
+                c += s_c[w][lane];
+                k += s_k[w][lane];
+            }
+            const float len = float(sp.hi > sp.lo ? sp.hi - sp.lo : 1);
+            const long long o = (long long)s * a.E + e;
+            a.cand[o] = c;
+            if (a.kept) a.kept[o] = k;
+            if (a.prob) a.prob[o] = p / len;
+            term = float(a.count_kept ? k : c) * float(a.E) / (float(a.K) * len) * (p / len);
+        }
+        term = warp_sum(term);
+        if (lane == 0) {
+            const int n = gridDim.x * gridDim.y;
+            a.seq_loss[s * gridDim.y + blockIdx.y] = sp.bad ? NAN : term;
+            __threadfence();
+            s_last = atomicAdd(a.ticket, 1) == n - 1;
+        }
     }
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    float v = 0.0f;  // thread e: sequences e, e + 256, ...; then a fixed tree
-    for (int q = e; q < a.S; q += 256) v += __ldcg(a.seq_loss + q);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    if (lane == 0) s_sum[warp] = v;
+    const int n = gridDim.x * gridDim.y;
+    float v = 0.0f;  // thread i: terms i, i + threads, ...; then a fixed tree
+    for (int q = threadIdx.x; q < n; q += blockDim.x) v += __ldcg(a.seq_loss + q);
+    v = warp_sum(v);
+    if (lane == 0) s_p[0][warp] = v;
     __syncthreads();
-    if (e == 0) {
-        v = 0.0f;
-        for (int w = 0; w < 8; ++w) v += s_sum[w];
-        *a.loss = a.coef / float(a.S) * v;
+    if (warp == 0) {
+        v = warp_sum(lane < warps ? s_p[0][lane] : 0.0f);
+        if (lane == 0) *a.loss = a.coef / float(a.S) * v;
     }
 }
 
-// A warp per token.  Tokens outside every sequence get zeros.
+// A warp takes a run of tokens, and its sequence's f once per sequence.
+// Tokens outside every sequence get zeros.
 template <int EPL>
 __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, E = a.E;
-    const int step = int(gridDim.x) * 8;
+    const int t0 = (int(blockIdx.x) * 8 + int(threadIdx.x >> 5)) * a.C, t1 = min(a.T, t0 + a.C);
+    if (t0 >= t1) return;
     const float up = a.coef / float(a.S) * (a.dloss ? *a.dloss : 1.0f);
-    for (int t = int(blockIdx.x) * 8 + (threadIdx.x >> 5); t < a.T; t += step) {
-        float r[EPL];
-        load_row(a.logits + (long long)t * a.ld, E, r);
-        // the first sequence that holds t (32 at a time)
-        int s = -1;
-        bool bad = false;
-        for (int s0 = 0; s0 < a.S && s < 0; s0 += 32) {
-            bool in = false;
-            if (s0 + lane < a.S) {
-                const Span sp = span_of(a, s0 + lane);
-                in = t >= sp.lo && t < sp.hi;
-                bad |= sp.bad;
+    float next[EPL], f[EPL];
+    load_row(a.logits + (long long)t0 * a.ld, E, next);
+    int s = first_ending_after(a, t0), ends = t0;  // f is of the tokens before `ends`
+    float g = 0.0f;
+    for (int t = t0; t < t1; ++t) {
+        if (t >= ends) {
+            Span sp = {t, t1, false};  // behind the last sequence: none
+            for (; s < a.S; ++s) {
+                sp = span_of(a, s);
+                if (sp.hi > t) break;
+                sp.lo = t;
+                sp.hi = t1;
             }
-            const unsigned b = __ballot_sync(kAll, in);
-            if (b) s = s0 + __ffs(b) - 1;
-        }
-        bad = __any_sync(kAll, bad);
-        float g = 0.0f, f[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) f[i] = 0.0f;
-        if (s >= 0) {
-            const Span sp = span_of(a, s);
+            const bool in = s < a.S && sp.lo <= t;
+            ends = in || s >= a.S ? sp.hi : sp.lo;
             const float len = float(sp.hi - sp.lo);
             const float scale = float(E) / (float(a.K) * len);
-            const int *c = a.counts + (long long)s * E;
+            g = in ? up / len : 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (lane + 32 * i < E) f[i] = float(c[lane + 32 * i]) * scale;
-            g = up / len;
+                f[i] = in && lane + 32 * i < E
+                           ? float(a.counts[(long long)s * E + lane + 32 * i]) * scale
+                           : 0.0f;
         }
-        softmax_row(r, E);
-        float dot = 0.0f;
+        float r[EPL], m = -INFINITY, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            r[i] = next[i];
+            m = fmaxf(m, r[i]);
+        }
+        if (t + 1 < t1) load_row(a.logits + (long long)(t + 1) * a.ld, E, next);
+        softmax_row(r, warp_max(m));
 #pragma unroll
         for (int i = 0; i < EPL; ++i) dot = fmaf(f[i], r[i], dot);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+        dot = warp_sum(dot);
         float *out = a.dlogits + (long long)t * E;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < E)
-                out[lane + 32 * i] = bad ? NAN : s < 0 ? 0.0f : g * r[i] * (f[i] - dot);
+            if (lane + 32 * i < E) out[lane + 32 * i] = g == 0.0f ? 0.0f : g * r[i] * (f[i] - dot);
     }
 }
 
 struct Layout {
-    int C, chunks;
+    int C, chunks, slabs;
     size_t off_p, off_c, off_k, off_loss, bytes;
 };
 
 Layout layout_of(const beam_balance_desc *d) {
     Layout l;
-    // about four CTAs per SM, at least two tokens per warp
-    long long c = (d->T + 4ll * kNominalSMs - 1) / (4ll * kNominalSMs);
+    // one wave of CTAs, at least two tokens per warp
+    const long long ctas = (d->E > 128 ? 3ll : 4ll) * kNominalSMs;
+    long long c = (d->T + ctas - 1) / ctas;
     c = (c + kBalWarps - 1) / kBalWarps * kBalWarps;
-    l.C = int(c < 2 * kBalWarps ? 2 * kBalWarps : c);
-    l.chunks = d->T / l.C + (d->n_seq < d->T ? d->n_seq : d->T);  // an unfilled one per sequence
-    const size_t n = size_t(l.chunks) * size_t(d->E) * 4;
+    l.C = int(c < 2 * kBalWarps ? 2 * kBalWarps : c > kMaxChunk ? kMaxChunk : c);
+    l.chunks = int((d->T + (long long)l.C - 1) / l.C);
+    l.slabs = (d->E + 31) / 32;
+    const size_t n = (size_t(l.chunks) + size_t(d->n_seq)) * size_t(d->E) * 4;
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     l.off_p = 256;
     l.off_c = up(l.off_p + n);
     l.off_k = up(l.off_c + n);
-    l.off_loss = up(l.off_k + n);
-    l.bytes = up(l.off_loss + 4 * size_t(d->n_seq));
+    l.off_loss = up(l.off_k + (d->has_mask ? n : 0));
+    l.bytes = up(l.off_loss + 4 * size_t(d->n_seq) * size_t(l.slabs));
     return l;
 }
 
@@ -335,8 +379,7 @@ beam_status check_balance_desc(const beam_balance_desc *d) {
     if (d->logits_ld < (d->has_mask ? 2 * d->E : d->E)) return BEAM_ERR_INVALID_ARG;
     if (d->mask_logit_threshold != d->mask_logit_threshold) return BEAM_ERR_INVALID_ARG;
     if (!(d->coef - d->coef == 0.0f)) return BEAM_ERR_INVALID_ARG;
-    // tokens are counted in 32 bits, with room for a grid's step; so are chunks,
-    // at most 593 a sequence even where boundaries make sequences overlap
+    // tokens and a chunk's end are counted in 32 bits
     if (d->T > 0x3fffffff || d->n_seq > (1 << 20)) return BEAM_ERR_UNSUPPORTED_SHAPE;
     return BEAM_OK;
 }
@@ -408,7 +451,6 @@ beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
     char *ws = static_cast<char *>(workspace);
     BalanceArgs a = balance_args(desc);
     a.C = l.C;
-    a.chunks = l.chunks;
     a.logits = logits;
     a.seq_begin = seq_begin;
     a.ticket = reinterpret_cast<int *>(ws);
@@ -422,7 +464,11 @@ beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
     a.prob = mean_prob;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = by_experts<Chunks>(desc->E, a, l.chunks > 0 ? l.chunks : 1, st);
-    if (e == cudaSuccess) e = launch_pdl(balance_final_kernel, dim3(desc->n_seq), dim3(256), 0, st, a);
+    // warps: about the parts of a sequence of mean length, 8 to 32
+    int warps = 8;
+    while (warps < 32 && (long long)warps * desc->n_seq < l.chunks) warps *= 2;
+    if (e == cudaSuccess)
+        e = launch_pdl(balance_final_kernel, dim3(desc->n_seq, l.slabs), dim3(32 * warps), 0, st, a);
     return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
 }
 
@@ -444,8 +490,11 @@ beam_status beam_moe_balance_backward(const beam_balance_desc *desc, const float
     a.counts = counts;
     a.dloss = dloss;
     a.dlogits = dlogits;
-    const long long blocks = (desc->T + 7ll) / 8, cap = 8ll * device_sm_count();
-    const cudaError_t e = by_experts<Grad>(desc->E, a, int(blocks < cap ? blocks : cap),
+    // a run of tokens per warp, eight CTAs per SM where there are as many
+    const long long warps = 64ll * device_sm_count();
+    a.C = int((desc->T + warps - 1) / warps);
+    const long long runs = (desc->T + (long long)a.C - 1) / a.C;
+    const cudaError_t e = by_experts<Grad>(desc->E, a, int((runs + 7) / 8),
                                            static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
 }

@@ -390,14 +390,14 @@ struct BlockArgs {
 struct BalanceArgs {
     int T, E, K, S, ld, has_mask, count_kept;
     float thr, coef;
-    int C, chunks;               // tokens per chunk, chunks there can be
+    int C;                       // tokens per chunk (backward: per warp)
     const float *logits;         // [T][ld]
     const int *seq_begin;        // [S + 1] or null (one sequence)
     float *loss, *prob;          // [1], [S][E]
     int *cand, *kept;            // [S][E]
     int *ticket;                 // sequences finished
-    float *part_p, *seq_loss;    // [chunks][E], [S]
-    int *part_c, *part_k;        // [chunks][E]
+    float *part_p, *seq_loss;    // [chunks + S][E], [S][slabs of 32 experts]
+    int *part_c, *part_k;        // [chunks + S][E]
     const int *counts;           // backward: [S][E]
     const float *dloss;          // [1] or null (1)
     float *dlogits;              // [T][E]

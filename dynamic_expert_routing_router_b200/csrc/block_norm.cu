@@ -144,13 +144,12 @@ __device__ __forceinline__ Vec<T> read_copy(const uint4 *slot, int plane_step) {
 }
 
 // ------------------------------------------------------------- row sums --
-// A row's warps.  `slot` counts its reductions: two buffers in turn let one
-// barrier per reduction do (a buffer is written again only after every warp
-// has passed the next reduction's barrier, so after it has read this one).
+// A row's warps, and two scratch buffers in turn, so that one barrier per
+// reduction does (a buffer is written again only after every warp has passed
+// the next reduction's barrier, so after it has read this one).
 struct Row {
     int warps, group, lane, warp;  // warps per row, group in the CTA, lane, warp in the group
-    float *scratch;                // this group's [2][warps][8]
-    int slot;
+    float *now, *next;             // [warps][8] each, of this group
 };
 
 __device__ __forceinline__ Row this_row(int warps, float *scratch) {
@@ -160,36 +159,30 @@ __device__ __forceinline__ Row this_row(int warps, float *scratch) {
     r.group = w / warps;
     r.warp = w - r.group * warps;
     r.lane = threadIdx.x & 31;
-    r.scratch = scratch + r.group * warps * 16;
-    r.slot = 0;
+    r.now = scratch + r.group * warps * 16;
+    r.next = r.now + warps * 8;
     return r;
 }
 
-__device__ __forceinline__ float *next_buffer(Row &r) {
-    float *s = r.scratch + (r.slot & 1) * r.warps * 8;
-    ++r.slot;
+// Every thread then reads the buffer this returns.
+__device__ __forceinline__ const float *shared_by_group(Row &r) {
+    asm volatile("bar.sync %0, %1;" ::"r"(r.group + 1), "r"(r.warps * 32) : "memory");
+    const float *s = r.now;
+    r.now = r.next;
+    r.next = const_cast<float *>(s);
     return s;
 }
-__device__ __forceinline__ void group_sync(const Row &r) {
-    asm volatile("bar.sync %0, %1;" ::"r"(r.group + 1), "r"(r.warps * 32) : "memory");
-}
 
-template <int N>
-__device__ __forceinline__ void row_sum(Row &r, float (&v)[N]) {
+__device__ __forceinline__ float row_sum(Row &r, float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    if (r.warps == 1) return v;
+    if (r.lane == 0) r.now[r.warp] = v;
+    const float *s = shared_by_group(r);
+    v = r.lane < r.warps ? s[r.lane] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], o);
-    if (r.warps == 1) return;
-    float *s = next_buffer(r);
-    if (r.lane < N) s[r.warp * 8 + r.lane] = r.lane == 0 ? v[0] : v[N - 1];
-    group_sync(r);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = r.lane < r.warps ? s[r.lane * 8 + i] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kAll, v[i], o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return __shfl_sync(kAll, v, 0);  // of lanes 0..15
 }
 
 // Eight sums at once: each exchange halves the values a lane carries, nine
@@ -207,135 +200,143 @@ __device__ __forceinline__ void row_sum8(Row &r, float (&v)[8]) {
     float t = v[0];  // of value lane / 4
     t += __shfl_xor_sync(kAll, t, 2);
     t += __shfl_xor_sync(kAll, t, 1);
+    int step = 4;
     if (r.warps > 1) {
-        float *s = next_buffer(r);
-        if ((r.lane & 3) == 0) s[r.warp * 8 + (r.lane >> 2)] = t;
-        group_sync(r);
+        if ((r.lane & 3) == 0) r.now[r.warp * 8 + (r.lane >> 2)] = t;
+        const float *s = shared_by_group(r);
         t = 0.0f;
         for (int w = r.lane >> 3; w < r.warps; w += 4) t += s[w * 8 + (r.lane & 7)];
         t += __shfl_xor_sync(kAll, t, 8);
         t += __shfl_xor_sync(kAll, t, 16);
+        step = 1;
     }
-    const int step = r.warps > 1 ? 1 : 4;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kAll, t, i * step);
 }
 
 // ------------------------------------------------------------- forward --
-// Weights stay in registers while a thread has one vector (NV = 1); the pair
-// w, gate_c is multiplied once.
+// Weights stay in registers where a thread has one or two vectors; the pair w,
+// gate_c is multiplied once.  A thread's fixed costs per row (addresses, two
+// reductions) are as large as the arithmetic of eight elements: hence up to
+// four vectors a thread, and 512 threads a CTA at most.
+constexpr int kThreads = 512;
+
 template <typename T, int NV, bool BRANCH>
-__global__ void __launch_bounds__(1024, 1)
+__global__ void __launch_bounds__(kThreads, NV <= 2 ? 2 : 1)
     block_forward_kernel(const BlockArgs a, const Ring ring, int warps) {
-    constexpr bool KEEP = NV == 1;
+    constexpr bool KEEP = NV <= 1 || (NV == 2 && sizeof(T) == 2);
+    constexpr int N = Vec<T>::N;
     extern __shared__ uint4 s_ring[];
-    __shared__ float scratch[2 * 32 * 8];
+    __shared__ float scratch[2 * 16 * 8];
     griddep_wait();
     griddep_launch_dependents();
     Row row = this_row(warps, scratch);
     const int groups = (blockDim.x >> 5) / warps;
-    const int d = a.d, lanes = warps * 32, me = row.warp * 32 + row.lane;
-    const float inv_d = 1.0f / float(d);
-    const T *x = static_cast<const T *>(a.x), *y = static_cast<const T *>(a.y);
+    const int lanes = warps * 32, me = row.warp * 32 + row.lane;
+    const float inv_d = 1.0f / float(a.d), eps = a.eps, res_scale = a.res_scale;
     const T *w = static_cast<const T *>(a.w), *gc = static_cast<const T *>(a.gc);
     const T *gt = static_cast<const T *>(a.gt), *wn = static_cast<const T *>(a.wn);
-    T *out = static_cast<T *>(a.out), *n = static_cast<T *>(a.n);
-    const long long step = (long long)gridDim.x * groups;
-    long long t = (long long)blockIdx.x * groups + row.group;
-    const int plane = NV * lanes, stage_step = ring.planes * plane;
-    uint4 *base = s_ring + row.group * ring.depth * stage_step + me;
-    auto fetch = [&](long long q, int stage) {
-        if (q < a.T) {
+    const unsigned step = gridDim.x * groups, rows = a.T;
+    unsigned t = blockIdx.x * groups + row.group;
+    const long long hop = (long long)step * a.d;
+    const int plane = NV * lanes, stage_step = ring.planes * plane, wrap = ring.depth * stage_step;
+    uint4 *const base = s_ring + row.group * wrap + me;
+    bool in[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = (i * lanes + me) * 8;
-                if (j >= d) continue;
-                uint4 *s = base + stage * stage_step + i * lanes;
-                copy_ahead(s, plane, x + q * d + j);
-                if (BRANCH) copy_ahead(s + Vec<T>::N * plane, plane, y + q * d + j);
-            }
+    for (int i = 0; i < NV; ++i) in[i] = (i * lanes + me) * 8 < a.d;
+    long long at = (long long)t * a.d + me * 8, ahead = at;
+    unsigned t_ahead = t;
+    auto fetch = [&](uint4 *slot) {
+        if (t_ahead < rows) {
+            const T *x = static_cast<const T *>(a.x) + ahead, *y = static_cast<const T *>(a.y) + ahead;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    copy_ahead(slot + i * lanes, plane, x + i * lanes * 8);
+                    if (BRANCH) copy_ahead(slot + (i * lanes + N * plane), plane, y + i * lanes * 8);
+                }
         }
         cp_async_commit();
+        t_ahead += step;
+        ahead += hop;
     };
-    for (int s = 0; s < ring.depth; ++s) fetch(t + s * step, s);
-    float2 mw[KEEP ? 4 : 1], nw[KEEP ? 4 : 1];
+    for (int s = 0; s < wrap; s += stage_step) fetch(base + s);
+    float2 mw[KEEP ? NV : 1][4], nw[KEEP ? NV : 1][4];
     if constexpr (KEEP) {
-        const int j = me * 8 < d ? me * 8 : 0;
-        weights_of(mw, w, gc, j);
-        weights_of(nw, wn, static_cast<const T *>(nullptr), j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = in[i] ? (i * lanes + me) * 8 : 0;
+            if (BRANCH) weights_of(mw[i], w, gc, j);
+            weights_of(nw[i], wn, static_cast<const T *>(nullptr), j);
+        }
     }
-    float gate = gt && t < a.T ? to_f(gt[t]) : 0.0f;
-    for (int stage = 0; t < a.T; t += step) {
-        const long long at = t * d;
+    float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
+    for (int stage = 0; t < rows; t += step, at += hop) {
         const float z = gate;
-        if (gt && t + step < a.T) gate = to_f(gt[t + step]);
+        if (gt && t + step < rows) gate = to_f(gt[t + step]);
         cp_async_wait(ring.depth - 1);
-        const uint4 *src = base + stage * stage_step;
+        uint4 *src = base + stage;
+        stage = stage + stage_step == wrap ? 0 : stage + stage_step;
         float s = a.branch_scale;
         if (BRANCH) {
             if (gt) s *= 1.0f / (1.0f + expf(-z));
             if (w) {
                 float2 yy = both(0.0f);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if ((i * lanes + me) * 8 >= d) continue;
-                    const Vec<T> v = read_copy<T>(src + Vec<T>::N * plane + i * lanes, plane);
+                for (int i = 0; i < NV; ++i)
+                    if (in[i]) {
+                        const Vec<T> v = read_copy<T>(src + (i * lanes + N * plane), plane);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
-                }
-                float sum[1] = {yy.x + yy.y};
-                row_sum(row, sum);
-                s *= rsqrtf(fmaf(sum[0], inv_d, a.eps));
+                        for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
+                    }
+                s *= rsqrtf(fmaf(row_sum(row, yy.x + yy.y), inv_d, eps));
             }
         }
         Vec<T> o[NV];
         float2 oo = both(0.0f);
+        T *out = static_cast<T *>(a.out) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (j >= d) continue;
-            o[i] = read_copy<T>(src + i * lanes, plane);
-            if (BRANCH) {
-                const Vec<T> v = read_copy<T>(src + Vec<T>::N * plane + i * lanes, plane);
-                float2 m[4], f[4];
-                if constexpr (KEEP) {
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                o[i] = read_copy<T>(src + i * lanes, plane);
+                if (BRANCH) {
+                    const Vec<T> v = read_copy<T>(src + (i * lanes + N * plane), plane);
+                    float2 m[4], f[4];
+                    if constexpr (KEEP) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) m[k] = mw[k];
-                } else {
-                    weights_of(m, w, gc, j);
+                        for (int k = 0; k < 4; ++k) m[k] = mw[i][k];
+                    } else {
+                        weights_of(m, w, gc, (i * lanes + me) * 8);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        f[k] = __ffma2_rn(both(res_scale), o[i].two(k),
+                                          __fmul2_rn(__fmul2_rn(m[k], both(s)), v.two(k)));
+                    o[i].set(f);
+                    store_vec(out + i * lanes * 8, o[i]);
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    f[k] = __ffma2_rn(both(a.res_scale), o[i].two(k),
-                                      __fmul2_rn(__fmul2_rn(m[k], both(s)), v.two(k)));
-                o[i].set(f);
-                store_vec(out + at + j, o[i]);
+                for (int k = 0; k < 4; ++k) oo = __ffma2_rn(o[i].two(k), o[i].two(k), oo);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) oo = __ffma2_rn(o[i].two(k), o[i].two(k), oo);
-        }
-        fetch(t + ring.depth * step, stage);
-        stage = stage + 1 == ring.depth ? 0 : stage + 1;
+        fetch(src);
         if (!wn) continue;
-        float sum[1] = {oo.x + oo.y};
-        row_sum(row, sum);
-        const float r = rsqrtf(fmaf(sum[0], inv_d, a.eps));
+        const float r = rsqrtf(fmaf(row_sum(row, oo.x + oo.y), inv_d, eps));
+        T *n = static_cast<T *>(a.n) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (j >= d) continue;
-            float2 f[4];
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                float2 f[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(o[i].two(k), both(r));
-            if constexpr (KEEP) {
+                for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(o[i].two(k), both(r));
+                if constexpr (KEEP) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(f[k], nw[k]);
-            } else {
-                times(f, wn + j);
+                    for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(f[k], nw[i][k]);
+                } else {
+                    times(f, wn + (i * lanes + me) * 8);
+                }
+                o[i].set(f);
+                store_vec(n + i * lanes * 8, o[i]);
             }
-            o[i].set(f);
-            store_vec(n + at + j, o[i]);
-        }
     }
 }
 
@@ -344,128 +345,138 @@ __global__ void __launch_bounds__(1024, 1)
 // are summed before r(out) is known.  A thread owns its columns for all its
 // rows; a CTA's groups add theirs up in order, and each CTA writes one slab
 // [2][d] (S, dw_next) that block_columns_kernel adds up in order.
-constexpr int kBwThreads = 768;  // 80 registers a thread
-
-template <typename T, int NV, bool BRANCH>
-__global__ void __launch_bounds__(kBwThreads, 1)
+// BRANCH: exit's (else enter's, whose out is x); NEXT: with w_next.
+template <typename T, int NV, bool BRANCH, bool NEXT>
+__global__ void __launch_bounds__(kThreads, 1)
     block_backward_kernel(const BlockArgs a, const Ring ring, int warps) {
-    constexpr bool KEEP = NV == 1;
+    constexpr bool KEEP = NV <= 2;
     extern __shared__ uint4 s_ring[];
-    __shared__ float scratch[2 * 24 * 8];
+    __shared__ float scratch[2 * 16 * 8];
     griddep_wait();
     griddep_launch_dependents();
     Row row = this_row(warps, scratch);
     const int groups = (blockDim.x >> 5) / warps;
     const int d = a.d, lanes = warps * 32, me = row.warp * 32 + row.lane;
-    const float inv_d = 1.0f / float(d);
-    const T *x = static_cast<const T *>(a.x), *y = static_cast<const T *>(a.y);
+    const float inv_d = 1.0f / float(d), eps = a.eps, res_scale = a.res_scale;
     const T *w = static_cast<const T *>(a.w), *gc = static_cast<const T *>(a.gc);
     const T *gt = static_cast<const T *>(a.gt), *wn = static_cast<const T *>(a.wn);
-    const T *dout = static_cast<const T *>(a.dout);
-    T *dres = static_cast<T *>(a.dres), *dy = static_cast<T *>(a.dy);
+    const bool has_g = BRANCH || a.dout != nullptr, ring_n = ring.at_n >= 0;
+    const unsigned step = gridDim.x * groups, rows = a.T;
+    unsigned t = blockIdx.x * groups + row.group;
+    const long long hop = (long long)step * d;
+    const int plane = NV * lanes, stage_step = ring.planes * plane, wrap = ring.depth * stage_step;
+    const int off_y = ring.at_y * plane, off_g = ring.at_g * plane, off_n = ring.at_n * plane;
+    uint4 *const base = s_ring + row.group * wrap + me;
+    bool in[NV];
     float2 cs[NV][4], cn[NV][4];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        in[i] = (i * lanes + me) * 8 < d;
 #pragma unroll
         for (int k = 0; k < 4; ++k) cs[i][k] = cn[i][k] = both(0.0f);
-    const long long step = (long long)gridDim.x * groups;
-    long long t = (long long)blockIdx.x * groups + row.group;
-    const int plane = NV * lanes, stage_step = ring.planes * plane;
-    uint4 *base = s_ring + row.group * ring.depth * stage_step + me;
-    auto fetch = [&](long long q, int stage) {
-        if (q < a.T) {
+    }
+    long long at = (long long)t * d + me * 8, ahead = at;
+    unsigned t_ahead = t;
+    auto fetch = [&](uint4 *slot) {
+        if (t_ahead < rows) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int j = (i * lanes + me) * 8;
-                if (j >= d) continue;
-                uint4 *s = base + stage * stage_step + i * lanes;
-                const long long at = q * d + j;
-                if (ring.at_x >= 0) copy_ahead(s + ring.at_x * plane, plane, x + at);
-                if (ring.at_y >= 0) copy_ahead(s + ring.at_y * plane, plane, y + at);
-                if (ring.at_g >= 0) copy_ahead(s + ring.at_g * plane, plane, dout + at);
-                if (ring.at_n >= 0) copy_ahead(s + ring.at_n * plane, plane, a.dn + at);
-            }
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    uint4 *s = slot + i * lanes;
+                    const long long q = ahead + i * lanes * 8;
+                    if (NEXT) copy_ahead(s, plane, static_cast<const T *>(a.x) + q);
+                    if (BRANCH) copy_ahead(s + off_y, plane, static_cast<const T *>(a.y) + q);
+                    if (has_g) copy_ahead(s + off_g, plane, static_cast<const T *>(a.dout) + q);
+                    if (NEXT && ring_n) copy_ahead(s + off_n, plane, a.dn + q);
+                }
         }
         cp_async_commit();
+        t_ahead += step;
+        ahead += hop;
     };
-    for (int s = 0; s < ring.depth; ++s) fetch(t + s * step, s);
-    float2 mw[KEEP ? 4 : 1], nw[KEEP ? 4 : 1];
+    for (int s = 0; s < wrap; s += stage_step) fetch(base + s);
+    float2 mw[KEEP ? NV : 1][4], nw[KEEP ? NV : 1][4];
     if constexpr (KEEP) {
-        const int j = me * 8 < d ? me * 8 : 0;
-        weights_of(mw, w, gc, j);
-        weights_of(nw, wn, static_cast<const T *>(nullptr), j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int j = in[i] ? (i * lanes + me) * 8 : 0;
+            if (BRANCH) weights_of(mw[i], w, gc, j);
+            if (NEXT) weights_of(nw[i], wn, static_cast<const T *>(nullptr), j);
+        }
     }
-    float gate = gt && t < a.T ? to_f(gt[t]) : 0.0f;
+    float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
     struct Pieces {
         Vec<T> o, y, g;
         Vec<float> n;
     };
-    // Columns j of the row, of arrays that are not there zeros.
-    auto read = [&](Pieces &c, const uint4 *s, long long at) {
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) c.o.p[i] = c.y.p[i] = c.g.p[i] = make_uint4(0u, 0u, 0u, 0u);
-        c.n.p[0] = c.n.p[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (wn) {
-            c.o = read_copy<T>(s + ring.at_x * plane, plane);
-            c.n = ring.at_n >= 0 ? read_copy<float>(s + ring.at_n * plane, plane)
-                                 : load_vec(a.dn + at);
+    auto read = [&](Pieces &c, const uint4 *s, long long q) {
+        if (NEXT) {
+            c.o = read_copy<T>(s, plane);
+            c.n = ring_n ? read_copy<float>(s + off_n, plane) : load_vec(a.dn + q);
         }
-        if (BRANCH) c.y = read_copy<T>(s + ring.at_y * plane, plane);
-        if (dout) c.g = read_copy<T>(s + ring.at_g * plane, plane);
+        if (BRANCH) c.y = read_copy<T>(s + off_y, plane);
+        if (has_g) {
+            c.g = read_copy<T>(s + off_g, plane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < Vec<T>::N; ++i) c.g.p[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
     };
-    for (int stage = 0; t < a.T; t += step) {
-        const long long at = t * d;
+    auto weights = [&](float2(&m)[4], float2(&p)[4], int i) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = mw[i][k];
+                p[k] = nw[i][k];
+            }
+        } else {
+            if (BRANCH) weights_of(m, w, gc, (i * lanes + me) * 8);
+            if (NEXT) weights_of(p, wn, static_cast<const T *>(nullptr), (i * lanes + me) * 8);
+        }
+    };
+    for (int stage = 0; t < rows; t += step, at += hop) {
         const float z = gate;
-        if (gt && t + step < a.T) gate = to_f(gt[t + step]);
+        if (gt && t + step < rows) gate = to_f(gt[t + step]);
         cp_async_wait(ring.depth - 1);
-        const uint4 *src = base + stage * stage_step;
+        uint4 *src = base + stage;
+        stage = stage + stage_step == wrap ? 0 : stage + stage_step;
         float2 q[6];
 #pragma unroll
         for (int k = 0; k < 6; ++k) q[k] = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (j >= d) continue;
-            Pieces c;
-            read(c, src + i * lanes, at + j);
-            float2 m[4], p[4];
-            if constexpr (KEEP) {
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                Pieces c;
+                read(c, src + i * lanes, at + i * lanes * 8);
+                float2 m[4], p[4];
+                weights(m, p, i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    m[k] = mw[k];
-                    p[k] = nw[k];
+                    float2 o, pk, yk, mk;
+                    if (NEXT) {
+                        o = c.o.two(k);
+                        pk = __fmul2_rn(p[k], c.n.two(k));
+                        q[0] = __ffma2_rn(o, o, q[0]);
+                        q[1] = __ffma2_rn(pk, o, q[1]);
+                    }
+                    if (BRANCH) {
+                        yk = c.y.two(k);
+                        mk = __fmul2_rn(m[k], yk);
+                        q[2] = __ffma2_rn(yk, yk, q[2]);
+                        q[3] = __ffma2_rn(mk, c.g.two(k), q[3]);
+                    }
+                    if (BRANCH && NEXT) {
+                        q[4] = __ffma2_rn(mk, pk, q[4]);
+                        q[5] = __ffma2_rn(mk, o, q[5]);
+                    }
                 }
-            } else {
-                weights_of(m, w, gc, j);
-                weights_of(p, wn, static_cast<const T *>(nullptr), j);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 o = c.o.two(k), pk = __fmul2_rn(p[k], c.n.two(k));
-                q[0] = __ffma2_rn(o, o, q[0]);
-                q[1] = __ffma2_rn(pk, o, q[1]);
-                if (BRANCH) {
-                    const float2 yk = c.y.two(k), mk = __fmul2_rn(m[k], yk);
-                    q[2] = __ffma2_rn(yk, yk, q[2]);
-                    q[3] = __ffma2_rn(mk, c.g.two(k), q[3]);
-                    q[4] = __ffma2_rn(mk, pk, q[4]);
-                    q[5] = __ffma2_rn(mk, o, q[5]);
-                }
-            }
-        }
         float sum[8];
-        if (BRANCH) {
 #pragma unroll
-            for (int k = 0; k < 6; ++k) sum[k] = q[k].x + q[k].y;
-            sum[6] = sum[7] = 0.0f;
-            row_sum8(row, sum);
-        } else {
-            float two[2] = {q[0].x + q[0].y, q[1].x + q[1].y};
-            row_sum(row, two);
-            sum[0] = two[0];
-            sum[1] = two[1];
-        }
-        const float ro = wn ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.0f;
+        for (int k = 0; k < 6; ++k) sum[k] = q[k].x + q[k].y;
+        sum[6] = sum[7] = 0.0f;
+        row_sum8(row, sum);
+        const float ro = NEXT ? rsqrtf(fmaf(sum[0], inv_d, eps)) : 0.0f;
         // mean(dn w o) of the formula, o normed; no power of r(out) above one
         // is formed, which tiny rows would take past fp32
         const float mo = ro * sum[1] * inv_d;
@@ -476,56 +487,49 @@ __global__ void __launch_bounds__(kBwThreads, 1)
                 sig = 1.0f / (1.0f + expf(-z));
                 rest = 1.0f / (1.0f + expf(z));
             }
-            if (w) ry = rsqrtf(fmaf(sum[2], inv_d, a.eps));
+            if (w) ry = rsqrtf(fmaf(sum[2], inv_d, eps));
             const float dot =
                 a.branch_scale * sig * ry * (sum[3] + ro * (sum[4] - mo * (ro * sum[5])));
-            if (w) back = dot * inv_d;
+            if (w) back = -dot * inv_d;
             if (gt && me == 0) a.dgt[t] = rest * dot;
         }
         const float zs = a.branch_scale * sig;
+        T *dres = static_cast<T *>(a.dres) + at, *dy = static_cast<T *>(a.dy) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (j >= d) continue;
-            Pieces c;
-            read(c, src + i * lanes, at + j);
-            float2 m[4], p[4], g[4], f[4];
-            if constexpr (KEEP) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    m[k] = mw[k];
-                    p[k] = nw[k];
-                }
-            } else {
-                weights_of(m, w, gc, j);
-                weights_of(p, wn, static_cast<const T *>(nullptr), j);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
-                const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p[k], n));
-                g[k] = __ffma2_rn(both(ro), u, c.g.two(k));
-                cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
-                f[k] = __fmul2_rn(both(a.res_scale), g[k]);
-            }
-            Vec<T> r;
-            r.set(f);
-            store_vec(dres + at + j, r);
-            if constexpr (BRANCH) {
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                Pieces c;
+                read(c, src + i * lanes, at + i * lanes * 8);
+                float2 m[4], p[4], g[4], f[4];
+                weights(m, p, i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 dz = __fmul2_rn(both(zs), g[k]);
-                    const float2 h = __fmul2_rn(c.y.two(k), both(ry));
-                    cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
-                    f[k] = __fmul2_rn(both(ry),
-                                      __ffma2_rn(dz, m[k], __fmul2_rn(h, both(-back))));
+                    g[k] = c.g.two(k);
+                    if (NEXT) {
+                        const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
+                        const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p[k], n));
+                        g[k] = __ffma2_rn(both(ro), u, g[k]);
+                        cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
+                    }
+                    f[k] = __fmul2_rn(both(res_scale), g[k]);
                 }
+                Vec<T> r;
                 r.set(f);
-                store_vec(dy + at + j, r);
+                store_vec(dres + i * lanes * 8, r);
+                if constexpr (BRANCH) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 dz = __fmul2_rn(both(zs), g[k]);
+                        const float2 h = __fmul2_rn(c.y.two(k), both(ry));
+                        cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
+                        f[k] = __fmul2_rn(both(ry),
+                                          __ffma2_rn(dz, m[k], __fmul2_rn(h, both(back))));
+                    }
+                    r.set(f);
+                    store_vec(dy + i * lanes * 8, r);
+                }
             }
-        }
-        fetch(t + ring.depth * step, stage);
-        stage = stage + 1 == ring.depth ? 0 : stage + 1;
+        fetch(src);
     }
     if (!a.part) return;
     // The CTA's slab: its groups in order, in what was the ring.
@@ -535,17 +539,17 @@ __global__ void __launch_bounds__(kBwThreads, 1)
         __syncthreads();
         if (row.group != g) continue;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int j = (i * lanes + me) * 8;
-            if (j >= d) continue;
+        for (int i = 0; i < NV; ++i)
+            if (in[i]) {
+                const int j = (i * lanes + me) * 8;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float2 *s = reinterpret_cast<float2 *>(s_cols + j + 2 * k);
-                float2 *n = reinterpret_cast<float2 *>(s_cols + d + j + 2 * k);
-                *s = g ? __fadd2_rn(*s, cs[i][k]) : cs[i][k];
-                *n = g ? __fadd2_rn(*n, cn[i][k]) : cn[i][k];
+                for (int k = 0; k < 4; ++k) {
+                    float2 *s = reinterpret_cast<float2 *>(s_cols + j + 2 * k);
+                    float2 *n = reinterpret_cast<float2 *>(s_cols + d + j + 2 * k);
+                    *s = g ? __fadd2_rn(*s, cs[i][k]) : cs[i][k];
+                    *n = g ? __fadd2_rn(*n, cn[i][k]) : cn[i][k];
+                }
             }
-        }
     }
     __syncthreads();
     float *slab = a.part + (long long)blockIdx.x * 2 * d;
@@ -605,18 +609,20 @@ struct Shape {
 
 Shape shape_of(const beam_block_desc *d, bool backward) {
     Shape s;
-    const int vecs = d->d / 8, most = backward ? kBwThreads : 1024;
-    s.nv = (vecs + most - 1) / most;
+    const int vecs = d->d / 8, rows = d->T / kNominalSMs;
+    s.nv = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+    // many rows per SM: fewer, busier warps; few: more warps, sooner done
+    if (s.nv == 1 && vecs >= 128 && rows >= 4) s.nv = 2;
     s.warps = (vecs + 32 * s.nv - 1) / (32 * s.nv);
     // Backward: one CTA per SM, so that there are few slabs.  Forward: CTAs of
     // at least four warps, several per SM.  Named barriers are 1..15.
-    s.groups = backward ? most / 32 / s.warps : s.warps < 4 ? 4 / s.warps : 1;
+    s.groups = backward ? kThreads / 32 / s.warps : s.warps < 4 ? 4 / s.warps : 1;
     if (s.groups > 15) s.groups = 15;
     // rather a row on every SM than several on a few
-    const int rows = d->T / kNominalSMs;
     if (s.groups > rows) s.groups = rows > 1 ? rows : 1;
     const int threads = s.groups * s.warps * 32;
-    s.per_sm = backward ? 1 : 1024 / threads < 8 ? 1024 / threads : 8;
+    const int resident = s.nv <= 2 ? 2 * kThreads : kThreads;
+    s.per_sm = backward ? 1 : resident / threads < 8 ? resident / threads : 8;
     const long long want = ((long long)d->T + s.groups - 1) / s.groups;
     const long long cap = (long long)kNominalSMs * s.per_sm;
     s.grid = int(want < cap ? want : cap);
@@ -673,13 +679,14 @@ cudaError_t launch_forward_nv(const BlockArgs &a, const Shape &s, cudaStream_t s
 
 template <typename T, bool BRANCH>
 cudaError_t launch_forward(const BlockArgs &a, const Shape &s, cudaStream_t st) {
-    return s.nv == 1 ? launch_forward_nv<T, 1, BRANCH>(a, s, st)
-                     : launch_forward_nv<T, 2, BRANCH>(a, s, st);
+    return s.nv == 1   ? launch_forward_nv<T, 1, BRANCH>(a, s, st)
+           : s.nv == 2 ? launch_forward_nv<T, 2, BRANCH>(a, s, st)
+                       : launch_forward_nv<T, 4, BRANCH>(a, s, st);
 }
 
-template <typename T, int NV, bool BRANCH>
+template <typename T, int NV, bool BRANCH, bool NEXT>
 cudaError_t launch_backward_nv(const BlockArgs &a, Shape s, cudaStream_t st) {
-    auto kern = block_backward_kernel<T, NV, BRANCH>;
+    auto kern = block_backward_kernel<T, NV, BRANCH, NEXT>;
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
     cudaError_t e = set_smem_once(kern, kSmemMost, attr_set);
     if (e != cudaSuccess) return e;
@@ -689,11 +696,11 @@ cudaError_t launch_backward_nv(const BlockArgs &a, Shape s, cudaStream_t st) {
     return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, r, s.warps);
 }
 
-template <typename T, bool BRANCH>
+template <typename T, bool BRANCH, bool NEXT>
 cudaError_t launch_backward(const BlockArgs &a, const Shape &s, cudaStream_t st) {
-    cudaError_t e = s.nv == 1   ? launch_backward_nv<T, 1, BRANCH>(a, s, st)
-                    : s.nv == 2 ? launch_backward_nv<T, 2, BRANCH>(a, s, st)
-                                : launch_backward_nv<T, 3, BRANCH>(a, s, st);
+    cudaError_t e = s.nv == 1   ? launch_backward_nv<T, 1, BRANCH, NEXT>(a, s, st)
+                    : s.nv == 2 ? launch_backward_nv<T, 2, BRANCH, NEXT>(a, s, st)
+                                : launch_backward_nv<T, 4, BRANCH, NEXT>(a, s, st);
     if (e != cudaSuccess || !a.part) return e;
     return launch_pdl(block_columns_kernel<T>, dim3((a.d + 31) / 32), dim3(256), 0, st, a, s.grid);
 }
@@ -818,8 +825,8 @@ beam_status beam_block_enter_backward(const beam_block_desc *desc, const void *x
     a.dwn = dw;
     a.part = static_cast<float *>(workspace);
     const Shape sh = shape_of(desc, true);
-    return done(desc->dtype == BEAM_BF16 ? launch_backward<__nv_bfloat16, false>(a, sh, st)
-                                         : launch_backward<float, false>(a, sh, st));
+    return done(desc->dtype == BEAM_BF16 ? launch_backward<__nv_bfloat16, false, true>(a, sh, st)
+                                         : launch_backward<float, false, true>(a, sh, st));
 }
 
 beam_status beam_block_exit_backward(const beam_block_desc *desc, const void *y, const void *out,
@@ -861,8 +868,11 @@ beam_status beam_block_exit_backward(const beam_block_desc *desc, const void *y,
     a.dwn = dw_next;
     a.part = dw_out || dgate_c || dw_next ? static_cast<float *>(workspace) : nullptr;
     const Shape sh = shape_of(desc, true);
-    return done(desc->dtype == BEAM_BF16 ? launch_backward<__nv_bfloat16, true>(a, sh, st)
-                                         : launch_backward<float, true>(a, sh, st));
+    if (desc->dtype == BEAM_BF16)
+        return done(w_next ? launch_backward<__nv_bfloat16, true, true>(a, sh, st)
+                           : launch_backward<__nv_bfloat16, true, false>(a, sh, st));
+    return done(w_next ? launch_backward<float, true, true>(a, sh, st)
+                       : launch_backward<float, true, false>(a, sh, st));
 }
 
 }  // extern "C"

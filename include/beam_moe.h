@@ -471,7 +471,8 @@ typedef struct {
 /* Forward.  logits f32 [T, logits_ld]; seq_begin int32 [n_seq + 1] (device) or
  * NULL (n_seq == 1: all T): sequence s is tokens [seq_begin[s],
  * seq_begin[s + 1]); tokens outside every sequence do not count.  Boundaries
- * that decrease or leave [0, T] make the loss NaN.
+ * that decrease or leave [0, T] make the loss NaN; the counts, P and the
+ * gradient are then of no use.  A NaN logit makes P and the loss NaN.
  * Written: loss f32 [1]; cand_counts int32 [n_seq, E]; kept_counts the same or
  * NULL (only with has_mask); mean_prob f32 [n_seq, E] (P) or NULL.  Sums run
  * in a fixed order.  Workspace 256-byte aligned; calls that may overlap need

@@ -77,32 +77,34 @@ __device__ __forceinline__ void load_row(const float *p, int E, float (&r)[EPL])
     for (int i = 0; i < EPL; ++i) r[i] = lane + 32 * i < E ? __ldcs(p + lane + 32 * i) : -INFINITY;
 }
 
-// r, whose largest value (NaN left out) is m, becomes the softmax of the row.
-// A row of -infinities has none: zeros.  NaN logits reach the sum as NaN.
+// r, whose largest value (NaN left out) is m, becomes the softmax of the row
+// but for the factor that is returned.  A row of -infinities has none: zeros.
+// NaN logits reach the sum as NaN.
 template <int EPL>
-__device__ __forceinline__ void softmax_row(float (&r)[EPL], float m) {
+__device__ __forceinline__ float softmax_row(float (&r)[EPL], float m) {
     float sum = 0.0f;
+    if (m == -INFINITY) m = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        r[i] = r[i] == -INFINITY ? 0.0f : expf(r[i] - m);
+        r[i] = expf(r[i] - m);
         sum += r[i];
     }
     sum = warp_sum(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) r[i] *= inv;
+    return sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
-// Bit i: expert lane + 32 i is among the K largest of the row (ties to the
-// lower id, NaN as -infinity); *m the largest.  Each lane sorts its values;
-// then the largest heads are taken off, all that are equal at once, until K
-// are: the last one is the K-th largest.
+// Which of the row's values are its K largest (ties to the lower id, NaN as
+// -infinity): those >= the value returned, or in *ties, where that would be
+// too many, bit i for expert lane + 32 i.  *m is the largest.  Each lane sorts
+// its values; then the largest heads are taken off, all that are equal at
+// once, until K are: the last one is the K-th largest.
 template <int EPL>
-__device__ __forceinline__ unsigned largest(const float (&r)[EPL], int E, int K, float *m) {
+__device__ __forceinline__ float kth_largest(const float (&r)[EPL], int E, int K, float *m,
+                                             unsigned *ties) {
     const int lane = threadIdx.x & 31;
-    float h[EPL], v[EPL];
+    float h[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) h[i] = v[i] = fmaxf(r[i], -INFINITY);
+    for (int i = 0; i < EPL; ++i) h[i] = fmaxf(r[i], -INFINITY);
     // odd-even merge sort, descending
 #pragma unroll
     for (int p = 1; p < EPL; p <<= 1)
@@ -117,41 +119,39 @@ __device__ __forceinline__ unsigned largest(const float (&r)[EPL], int E, int K,
                         h[i + j] = fmaxf(x, y);
                         h[i + j + k] = fminf(x, y);
                     }
-    float kth = 0.0f;
-    int got = 0;
-    for (int k = 0; k < K && got < K; ++k) {
-        kth = warp_max(h[0]);
-        if (k == 0) *m = kth;
+    float kth = warp_max(h[0]);
+    *m = kth;
+    for (int got = 0;;) {
         const bool mine = h[0] == kth;
         got += __popc(__ballot_sync(kAll, mine));
-        if (mine) {
 #pragma unroll
-            for (int i = 0; i + 1 < EPL; ++i) h[i] = h[i + 1];
-            h[EPL - 1] = -INFINITY;
+        for (int i = 0; i + 1 < EPL; ++i) h[i] = mine ? h[i + 1] : h[i];
+        h[EPL - 1] = mine ? -INFINITY : h[EPL - 1];
+        const float next = warp_max(h[0]);
+        if (got >= K) {
+            // Exactly K reach the K-th.  (Equal values of one lane come off
+            // one by one, so one may be left.)
+            *ties = 0u;
+            if (got == K && next != kth && kth != -INFINITY) return kth;
+            break;
         }
-    }
-    unsigned taken = 0;
-    // Exactly K values reach the K-th: they are the ones.  (Equal heads of one
-    // lane come off one by one, so look whether one more is left.)
-    if (got == K && kth != -INFINITY && !__any_sync(kAll, h[0] == kth)) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) taken |= v[i] >= kth ? 1u << i : 0u;
-        return taken;
+        kth = next;
     }
     // Ties: those above, then the lowest ids of the equal ones.
-    int more = 0;
+    int left = K;
+    unsigned taken = 0u;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) more += __popc(__ballot_sync(kAll, v[i] > kth));
-    int left = K - more;
+    for (int i = 0; i < EPL; ++i) left -= __popc(__ballot_sync(kAll, r[i] > kth));
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const bool tie = lane + 32 * i < E && v[i] == kth;
+        const bool tie = lane + 32 * i < E && fmaxf(r[i], -INFINITY) == kth;
         const unsigned b = __ballot_sync(kAll, tie);
         const int before = __popc(b & ((1u << lane) - 1u));
-        if (v[i] > kth || (tie && before < left)) taken |= 1u << i;
+        if (r[i] > kth || (tie && before < left)) taken |= 1u << i;
         left -= min(left, __popc(b));
     }
-    return taken;
+    *ties = taken;
+    return NAN;  // nothing reaches it
 }
 
 template <int EPL>
@@ -177,30 +177,36 @@ __global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
             acc[i] = 0.0f;
             count[i] = 0u;
         }
-        float next[EPL], znext[EPL];
-        auto load = [&](int t) {
-            const float *row = a.logits + (long long)t * a.ld;
-            load_row(row, E, next);
-            if (mask) load_row(row + E, E, znext);
-        };
+        float r[EPL], next[EPL];
         int t = lo + warp;
-        if (t < hi) load(t);
+        if (t < hi) load_row(a.logits + (long long)t * a.ld, E, r);
         for (; t < hi; t += kBalWarps) {
-            float r[EPL], z[EPL];
+            const float *row = a.logits + (long long)t * a.ld;
+            float z[EPL];
+            if (mask) load_row(row + E, E, z);
+            if (t + kBalWarps < hi) load_row(row + (long long)kBalWarps * a.ld, E, next);
+            float m;
+            unsigned ties;
+            const float kth = kth_largest(r, E, a.K, &m, &ties);
+            if (ties) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if ((ties >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
+            } else if (mask) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (r[i] >= kth) count[i] += z[i] >= a.thr ? 0x10001u : 1u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (r[i] >= kth) count[i] += 1u;
+            }
+            const float inv = softmax_row(r, m);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
+                acc[i] = fmaf(r[i], inv, acc[i]);
                 r[i] = next[i];
-                z[i] = znext[i];
             }
-            if (t + kBalWarps < hi) load(t + kBalWarps);
-            float m;
-            const unsigned taken = largest(r, E, a.K, &m);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if ((taken >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
-            softmax_row(r, m);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) acc[i] += r[i];
         }
         __syncthreads();  // the previous sequence's sums are out
 #pragma unroll
@@ -334,9 +340,12 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) 
             m = fmaxf(m, r[i]);
         }
         if (t + 1 < t1) load_row(a.logits + (long long)(t + 1) * a.ld, E, next);
-        softmax_row(r, warp_max(m));
+        const float inv = softmax_row(r, warp_max(m));
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) dot = fmaf(f[i], r[i], dot);
+        for (int i = 0; i < EPL; ++i) {
+            r[i] *= inv;
+            dot = fmaf(f[i], r[i], dot);
+        }
         dot = warp_sum(dot);
         float *out = a.dlogits + (long long)t * E;
 #pragma unroll

@@ -103,43 +103,35 @@ __device__ __forceinline__ void weights_of(float2 (&v)[4], const T *a, const T *
 }
 
 // ---------------------------------------------------------- loads ahead --
-// Shared memory of one group: [depth][planes][NV][lanes] 16-byte pieces, the
-// planes of a stage being those of the arrays it loads.
-struct Ring {
-    int depth, planes;
-    int at_x, at_y, at_g, at_n;  // first plane of each array; < 0: not loaded
-};
+// Shared memory of a CTA: [depth][pieces][CTA's threads at most] 16-byte
+// pieces.  A stage's pieces are those of one row's arrays, NV vectors each;
+// strides are the same for every launch of a kernel, so that a piece's address
+// is a constant from its stage's.  A thread whose last columns lie behind the
+// row finds zeros there, so only its copies and stores are left out.
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
 // Until at most `left` of the thread's copies (one group per row) are open.
-__device__ __forceinline__ void cp_async_wait(int left) {
+__device__ __forceinline__ void cp_async_wait_for(int left) {
     if (left == 0)
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        cp_async_wait<0>();
     else if (left == 1)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        cp_async_wait<1>();
     else if (left == 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        cp_async_wait<2>();
     else
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
+        cp_async_wait<3>();
 }
 
-template <typename T>
-__device__ __forceinline__ void copy_ahead(uint4 *slot, int plane_step, const T *src) {
+template <int THREADS, typename T>
+__device__ __forceinline__ void copy_ahead(uint4 *piece, const T *src) {
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i)
-        cp_async16(slot + i * plane_step, reinterpret_cast<const uint4 *>(src) + i);
+        cp_async_16(piece + i * THREADS, reinterpret_cast<const uint4 *>(src) + i);
 }
-template <typename T>
-__device__ __forceinline__ Vec<T> read_copy(const uint4 *slot, int plane_step) {
+template <int THREADS, typename T>
+__device__ __forceinline__ Vec<T> read_copy(const uint4 *piece) {
     Vec<T> v;
 #pragma unroll
-    for (int i = 0; i < Vec<T>::N; ++i) v.p[i] = slot[i * plane_step];
+    for (int i = 0; i < Vec<T>::N; ++i) v.p[i] = piece[i * THREADS];
     return v;
 }
 
@@ -182,7 +174,7 @@ __device__ __forceinline__ float row_sum(Row &r, float v) {
     v = r.lane < r.warps ? s[r.lane] : 0.0f;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    return __shfl_sync(kAll, v, 0);  // of lanes 0..15
+    return __shfl_sync(kAll, v, 0);  // of lanes 0..15: at most 16 warps
 }
 
 // Eight sums at once: each exchange halves the values a lane carries, nine
@@ -218,14 +210,20 @@ __device__ __forceinline__ void row_sum8(Row &r, float (&v)[8]) {
 // Weights stay in registers where a thread has one or two vectors; the pair w,
 // gate_c is multiplied once.  A thread's fixed costs per row (addresses, two
 // reductions) are as large as the arithmetic of eight elements: hence up to
-// four vectors a thread, and 512 threads a CTA at most.
-constexpr int kThreads = 512;
+// four vectors a thread.  Two CTAs of 448 threads leave a thread 72 registers,
+// which hold two bf16 vectors' state; with 512 (64 registers) some of it
+// spilled.
+template <int NV>
+constexpr int kFwThreads = NV <= 2 ? 448 : 512;
 
 template <typename T, int NV, bool BRANCH>
-__global__ void __launch_bounds__(kThreads, NV <= 2 ? 2 : 1)
-    block_forward_kernel(const BlockArgs a, const Ring ring, int warps) {
+__global__ void __launch_bounds__(kFwThreads<NV>, NV <= 2 ? 2 : 1)
+    block_forward_kernel(const BlockArgs a, int depth, int warps) {
+    constexpr int THREADS = kFwThreads<NV>;
     constexpr bool KEEP = NV <= 1 || (NV == 2 && sizeof(T) == 2);
     constexpr int N = Vec<T>::N;
+    constexpr int kVec = N * THREADS, kY = NV * kVec;  // next vector's pieces, y's first
+    constexpr int kStage = (BRANCH ? 2 : 1) * NV * kVec;
     extern __shared__ uint4 s_ring[];
     __shared__ float scratch[2 * 16 * 8];
     griddep_wait();
@@ -239,56 +237,61 @@ __global__ void __launch_bounds__(kThreads, NV <= 2 ? 2 : 1)
     const unsigned step = gridDim.x * groups, rows = a.T;
     unsigned t = blockIdx.x * groups + row.group;
     const long long hop = (long long)step * a.d;
-    const int plane = NV * lanes, stage_step = ring.planes * plane, wrap = ring.depth * stage_step;
-    uint4 *const base = s_ring + row.group * wrap + me;
+    uint4 *const base = s_ring + threadIdx.x;
+    const int wrap = depth * kStage;
     bool in[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) in[i] = (i * lanes + me) * 8 < a.d;
+    for (int i = 0; i < NV; ++i) {
+        in[i] = (i * lanes + me) * 8 < a.d;
+        if (!in[i])
+            for (int s = 0; s < wrap; s += kStage)
+#pragma unroll
+                for (int q = 0; q < (BRANCH ? 2 : 1) * N; ++q)
+                    base[s + (q / N) * kY + i * kVec + (q % N) * THREADS] = make_uint4(0u, 0u, 0u, 0u);
+    }
     long long at = (long long)t * a.d + me * 8, ahead = at;
     unsigned t_ahead = t;
-    auto fetch = [&](uint4 *slot) {
+    auto fetch = [&](int stage) {
         if (t_ahead < rows) {
             const T *x = static_cast<const T *>(a.x) + ahead, *y = static_cast<const T *>(a.y) + ahead;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i]) {
-                    copy_ahead(slot + i * lanes, plane, x + i * lanes * 8);
-                    if (BRANCH) copy_ahead(slot + (i * lanes + N * plane), plane, y + i * lanes * 8);
+                    copy_ahead<THREADS>(base + stage + i * kVec, x + i * lanes * 8);
+                    if (BRANCH) copy_ahead<THREADS>(base + stage + kY + i * kVec, y + i * lanes * 8);
                 }
         }
         cp_async_commit();
         t_ahead += step;
         ahead += hop;
     };
-    for (int s = 0; s < wrap; s += stage_step) fetch(base + s);
-    float2 mw[KEEP ? NV : 1][4], nw[KEEP ? NV : 1][4];
+    for (int s = 0; s < wrap; s += kStage) fetch(s);
+    float2 mw[KEEP ? NV : 1][4];
+    Vec<T> nw[KEEP ? NV : 1];
+    auto column = [&](int i) { return in[i] ? (i * lanes + me) * 8 : 0; };
     if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = in[i] ? (i * lanes + me) * 8 : 0;
-            if (BRANCH) weights_of(mw[i], w, gc, j);
-            weights_of(nw[i], wn, static_cast<const T *>(nullptr), j);
+            if (BRANCH) weights_of(mw[i], w, gc, column(i));
+            if (wn) nw[i] = load_vec(wn + column(i));
         }
     }
     float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
     for (int stage = 0; t < rows; t += step, at += hop) {
         const float z = gate;
         if (gt && t + step < rows) gate = to_f(gt[t + step]);
-        cp_async_wait(ring.depth - 1);
-        uint4 *src = base + stage;
-        stage = stage + stage_step == wrap ? 0 : stage + stage_step;
+        cp_async_wait_for(depth - 1);
         float s = a.branch_scale;
         if (BRANCH) {
             if (gt) s *= 1.0f / (1.0f + expf(-z));
             if (w) {
                 float2 yy = both(0.0f);
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (in[i]) {
-                        const Vec<T> v = read_copy<T>(src + (i * lanes + N * plane), plane);
+                for (int i = 0; i < NV; ++i) {
+                    const Vec<T> v = read_copy<THREADS, T>(base + stage + kY + i * kVec);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
-                    }
+                    for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
+                }
                 s *= rsqrtf(fmaf(row_sum(row, yy.x + yy.y), inv_d, eps));
             }
         }
@@ -296,47 +299,46 @@ __global__ void __launch_bounds__(kThreads, NV <= 2 ? 2 : 1)
         float2 oo = both(0.0f);
         T *out = static_cast<T *>(a.out) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
-                o[i] = read_copy<T>(src + i * lanes, plane);
-                if (BRANCH) {
-                    const Vec<T> v = read_copy<T>(src + (i * lanes + N * plane), plane);
-                    float2 m[4], f[4];
-                    if constexpr (KEEP) {
+        for (int i = 0; i < NV; ++i) {
+            o[i] = read_copy<THREADS, T>(base + stage + i * kVec);
+            if (BRANCH) {
+                const Vec<T> v = read_copy<THREADS, T>(base + stage + kY + i * kVec);
+                float2 m[4], f[4];
+                if constexpr (KEEP) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) m[k] = mw[i][k];
-                    } else {
-                        weights_of(m, w, gc, (i * lanes + me) * 8);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        f[k] = __ffma2_rn(both(res_scale), o[i].two(k),
-                                          __fmul2_rn(__fmul2_rn(m[k], both(s)), v.two(k)));
-                    o[i].set(f);
-                    store_vec(out + i * lanes * 8, o[i]);
+                    for (int k = 0; k < 4; ++k) m[k] = mw[i][k];
+                } else {
+                    weights_of(m, w, gc, column(i));
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) oo = __ffma2_rn(o[i].two(k), o[i].two(k), oo);
+                for (int k = 0; k < 4; ++k)
+                    f[k] = __ffma2_rn(both(res_scale), o[i].two(k),
+                                      __fmul2_rn(__fmul2_rn(m[k], both(s)), v.two(k)));
+                o[i].set(f);
+                if (in[i]) store_vec(out + i * lanes * 8, o[i]);
             }
-        fetch(src);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) oo = __ffma2_rn(o[i].two(k), o[i].two(k), oo);
+        }
+        fetch(stage);
+        stage = stage + kStage == wrap ? 0 : stage + kStage;
         if (!wn) continue;
         const float r = rsqrtf(fmaf(row_sum(row, oo.x + oo.y), inv_d, eps));
         T *n = static_cast<T *>(a.n) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
-                float2 f[4];
+        for (int i = 0; i < NV; ++i) {
+            float2 f[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(o[i].two(k), both(r));
-                if constexpr (KEEP) {
+            for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(o[i].two(k), both(r));
+            if constexpr (KEEP) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(f[k], nw[i][k]);
-                } else {
-                    times(f, wn + (i * lanes + me) * 8);
-                }
-                o[i].set(f);
-                store_vec(n + i * lanes * 8, o[i]);
+                for (int k = 0; k < 4; ++k) f[k] = __fmul2_rn(f[k], nw[i].two(k));
+            } else {
+                times(f, wn + column(i));
             }
+            o[i].set(f);
+            if (in[i]) store_vec(n + i * lanes * 8, o[i]);
+        }
     }
 }
 
@@ -346,12 +348,24 @@ __global__ void __launch_bounds__(kThreads, NV <= 2 ? 2 : 1)
 // rows; a CTA's groups add theirs up in order, and each CTA writes one slab
 // [2][d] (S, dw_next) that block_columns_kernel adds up in order.
 // BRANCH: exit's (else enter's, whose out is x); NEXT: with w_next.
+#ifndef BW1
+#define BW1 768
+#define BW2 512
+#endif
+template <int NV>
+constexpr int kBwThreads = NV == 1 ? BW1 : NV == 2 ? BW2 : 512;
+
 template <typename T, int NV, bool BRANCH, bool NEXT>
-__global__ void __launch_bounds__(kThreads, 1)
-    block_backward_kernel(const BlockArgs a, const Ring ring, int warps) {
+__global__ void __launch_bounds__(kBwThreads<NV>, 1)
+    block_backward_kernel(const BlockArgs a, int depth, int ring_n, int warps) {
+    constexpr int THREADS = kBwThreads<NV>;
     constexpr bool KEEP = NV <= 2;
+    constexpr int N = Vec<T>::N, kVec = N * THREADS;
+    constexpr int kY = NEXT ? NV * kVec : 0, kG = kY + (BRANCH ? NV * kVec : 0), kN = kG + NV * kVec;
+    constexpr int kStage = kN + (NEXT ? NV * 2 * THREADS : 0);
+    constexpr bool ALWAYS = NV < 4 || sizeof(T) == 2;  // dn is copied too
     extern __shared__ uint4 s_ring[];
-    __shared__ float scratch[2 * 16 * 8];
+    __shared__ float scratch[2 * (THREADS / 32) * 8];
     griddep_wait();
     griddep_launch_dependents();
     Row row = this_row(warps, scratch);
@@ -360,13 +374,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float inv_d = 1.0f / float(d), eps = a.eps, res_scale = a.res_scale;
     const T *w = static_cast<const T *>(a.w), *gc = static_cast<const T *>(a.gc);
     const T *gt = static_cast<const T *>(a.gt), *wn = static_cast<const T *>(a.wn);
-    const bool has_g = BRANCH || a.dout != nullptr, ring_n = ring.at_n >= 0;
+    const bool has_g = BRANCH || a.dout != nullptr;
     const unsigned step = gridDim.x * groups, rows = a.T;
     unsigned t = blockIdx.x * groups + row.group;
     const long long hop = (long long)step * d;
-    const int plane = NV * lanes, stage_step = ring.planes * plane, wrap = ring.depth * stage_step;
-    const int off_y = ring.at_y * plane, off_g = ring.at_g * plane, off_n = ring.at_n * plane;
-    uint4 *const base = s_ring + row.group * wrap + me;
+    uint4 *const base = s_ring + threadIdx.x;
+    // dn is the last array of a stage, and of all where it is not copied
+    const int stage_step = ALWAYS || ring_n ? kStage : kN, wrap = depth * stage_step;
     bool in[NV];
     float2 cs[NV][4], cn[NV][4];
 #pragma unroll
@@ -374,34 +388,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         in[i] = (i * lanes + me) * 8 < d;
 #pragma unroll
         for (int k = 0; k < 4; ++k) cs[i][k] = cn[i][k] = both(0.0f);
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int s = 0; s < wrap; s += stage_step) {
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const int at = s + i * kVec + q * THREADS;
+                if (!in[i] && NEXT) base[at] = zero;
+                if (!in[i] && BRANCH) base[at + kY] = zero;
+                if (!in[i] || !has_g) base[at + kG] = zero;
+            }
+            if (NEXT && !in[i] && (ALWAYS || ring_n))
+                base[s + kN + i * 2 * THREADS] = base[s + kN + i * 2 * THREADS + THREADS] = zero;
+        }
     }
     long long at = (long long)t * d + me * 8, ahead = at;
     unsigned t_ahead = t;
-    auto fetch = [&](uint4 *slot) {
+    auto fetch = [&](int stage) {
         if (t_ahead < rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i]) {
-                    uint4 *s = slot + i * lanes;
                     const long long q = ahead + i * lanes * 8;
-                    if (NEXT) copy_ahead(s, plane, static_cast<const T *>(a.x) + q);
-                    if (BRANCH) copy_ahead(s + off_y, plane, static_cast<const T *>(a.y) + q);
-                    if (has_g) copy_ahead(s + off_g, plane, static_cast<const T *>(a.dout) + q);
-                    if (NEXT && ring_n) copy_ahead(s + off_n, plane, a.dn + q);
+                    uint4 *to = base + stage + i * kVec;
+                    if (NEXT) copy_ahead<THREADS>(to, static_cast<const T *>(a.x) + q);
+                    if (BRANCH) copy_ahead<THREADS>(to + kY, static_cast<const T *>(a.y) + q);
+                    if (has_g) copy_ahead<THREADS>(to + kG, static_cast<const T *>(a.dout) + q);
+                    if (NEXT && (ALWAYS || ring_n))
+                        copy_ahead<THREADS>(base + stage + kN + i * 2 * THREADS, a.dn + q);
                 }
         }
         cp_async_commit();
         t_ahead += step;
         ahead += hop;
     };
-    for (int s = 0; s < wrap; s += stage_step) fetch(base + s);
-    float2 mw[KEEP ? NV : 1][4], nw[KEEP ? NV : 1][4];
+    for (int s = 0; s < wrap; s += stage_step) fetch(s);
+    float2 mw[KEEP ? NV : 1][4];
+    Vec<T> nw[KEEP ? NV : 1];
+    auto column = [&](int i) { return in[i] ? (i * lanes + me) * 8 : 0; };
     if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int j = in[i] ? (i * lanes + me) * 8 : 0;
-            if (BRANCH) weights_of(mw[i], w, gc, j);
-            if (NEXT) weights_of(nw[i], wn, static_cast<const T *>(nullptr), j);
+            if (BRANCH) weights_of(mw[i], w, gc, column(i));
+            if (NEXT) nw[i] = load_vec(wn + column(i));
         }
     }
     float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
@@ -409,68 +437,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         Vec<T> o, y, g;
         Vec<float> n;
     };
-    auto read = [&](Pieces &c, const uint4 *s, long long q) {
+    auto read = [&](Pieces &c, int stage, int i) {
+        const uint4 *from = base + stage + i * kVec;
         if (NEXT) {
-            c.o = read_copy<T>(s, plane);
-            c.n = ring_n ? read_copy<float>(s + off_n, plane) : load_vec(a.dn + q);
+            c.o = read_copy<THREADS, T>(from);
+            if (ALWAYS || ring_n)
+                c.n = read_copy<THREADS, float>(base + stage + kN + i * 2 * THREADS);
+            else if (in[i])
+                c.n = load_vec(a.dn + at + i * lanes * 8);
+            else
+                c.n.p[0] = c.n.p[1] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (BRANCH) c.y = read_copy<T>(s + off_y, plane);
-        if (has_g) {
-            c.g = read_copy<T>(s + off_g, plane);
-        } else {
-#pragma unroll
-            for (int i = 0; i < Vec<T>::N; ++i) c.g.p[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
+        if (BRANCH) c.y = read_copy<THREADS, T>(from + kY);
+        c.g = read_copy<THREADS, T>(from + kG);
     };
-    auto weights = [&](float2(&m)[4], float2(&p)[4], int i) {
+    auto weights = [&](float2(&m)[4], Vec<T> &p, int i) {
         if constexpr (KEEP) {
+            p = nw[i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                m[k] = mw[i][k];
-                p[k] = nw[i][k];
-            }
+            for (int k = 0; k < 4; ++k) m[k] = mw[i][k];
         } else {
-            if (BRANCH) weights_of(m, w, gc, (i * lanes + me) * 8);
-            if (NEXT) weights_of(p, wn, static_cast<const T *>(nullptr), (i * lanes + me) * 8);
+            if (BRANCH) weights_of(m, w, gc, column(i));
+            if (NEXT) p = load_vec(wn + column(i));
         }
     };
     for (int stage = 0; t < rows; t += step, at += hop) {
         const float z = gate;
         if (gt && t + step < rows) gate = to_f(gt[t + step]);
-        cp_async_wait(ring.depth - 1);
-        uint4 *src = base + stage;
-        stage = stage + stage_step == wrap ? 0 : stage + stage_step;
+        cp_async_wait_for(depth - 1);
         float2 q[6];
 #pragma unroll
         for (int k = 0; k < 6; ++k) q[k] = both(0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
-                Pieces c;
-                read(c, src + i * lanes, at + i * lanes * 8);
-                float2 m[4], p[4];
-                weights(m, p, i);
+        for (int i = 0; i < NV; ++i) {
+            Pieces c;
+            read(c, stage, i);
+            float2 m[4];
+            Vec<T> p;
+            weights(m, p, i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float2 o, pk, yk, mk;
-                    if (NEXT) {
-                        o = c.o.two(k);
-                        pk = __fmul2_rn(p[k], c.n.two(k));
-                        q[0] = __ffma2_rn(o, o, q[0]);
-                        q[1] = __ffma2_rn(pk, o, q[1]);
-                    }
-                    if (BRANCH) {
-                        yk = c.y.two(k);
-                        mk = __fmul2_rn(m[k], yk);
-                        q[2] = __ffma2_rn(yk, yk, q[2]);
-                        q[3] = __ffma2_rn(mk, c.g.two(k), q[3]);
-                    }
-                    if (BRANCH && NEXT) {
-                        q[4] = __ffma2_rn(mk, pk, q[4]);
-                        q[5] = __ffma2_rn(mk, o, q[5]);
-                    }
+            for (int k = 0; k < 4; ++k) {
+                float2 o, pk, yk, mk;
+                if (NEXT) {
+                    o = c.o.two(k);
+                    pk = __fmul2_rn(p.two(k), c.n.two(k));
+                    q[0] = __ffma2_rn(o, o, q[0]);
+                    q[1] = __ffma2_rn(pk, o, q[1]);
+                }
+                if (BRANCH) {
+                    yk = c.y.two(k);
+                    mk = __fmul2_rn(m[k], yk);
+                    q[2] = __ffma2_rn(yk, yk, q[2]);
+                    q[3] = __ffma2_rn(mk, c.g.two(k), q[3]);
+                }
+                if (BRANCH && NEXT) {
+                    q[4] = __ffma2_rn(mk, pk, q[4]);
+                    q[5] = __ffma2_rn(mk, o, q[5]);
                 }
             }
+        }
         float sum[8];
 #pragma unroll
         for (int k = 0; k < 6; ++k) sum[k] = q[k].x + q[k].y;
@@ -496,44 +521,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float zs = a.branch_scale * sig;
         T *dres = static_cast<T *>(a.dres) + at, *dy = static_cast<T *>(a.dy) + at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
-                Pieces c;
-                read(c, src + i * lanes, at + i * lanes * 8);
-                float2 m[4], p[4], g[4], f[4];
-                weights(m, p, i);
+        for (int i = 0; i < NV; ++i) {
+            Pieces c;
+            read(c, stage, i);
+            float2 m[4], g[4], f[4];
+            Vec<T> p;
+            weights(m, p, i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                g[k] = c.g.two(k);
+                if (NEXT) {
+                    const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
+                    const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p.two(k), n));
+                    g[k] = __ffma2_rn(both(ro), u, g[k]);
+                    cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
+                }
+                f[k] = __fmul2_rn(both(res_scale), g[k]);
+            }
+            Vec<T> r;
+            r.set(f);
+            if (in[i]) store_vec(dres + i * lanes * 8, r);
+            if constexpr (BRANCH) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    g[k] = c.g.two(k);
-                    if (NEXT) {
-                        const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
-                        const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p[k], n));
-                        g[k] = __ffma2_rn(both(ro), u, g[k]);
-                        cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
-                    }
-                    f[k] = __fmul2_rn(both(res_scale), g[k]);
+                    const float2 dz = __fmul2_rn(both(zs), g[k]);
+                    const float2 h = __fmul2_rn(c.y.two(k), both(ry));
+                    cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
+                    f[k] = __fmul2_rn(both(ry), __ffma2_rn(dz, m[k], __fmul2_rn(h, both(back))));
                 }
-                Vec<T> r;
                 r.set(f);
-                store_vec(dres + i * lanes * 8, r);
-                if constexpr (BRANCH) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 dz = __fmul2_rn(both(zs), g[k]);
-                        const float2 h = __fmul2_rn(c.y.two(k), both(ry));
-                        cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
-                        f[k] = __fmul2_rn(both(ry),
-                                          __ffma2_rn(dz, m[k], __fmul2_rn(h, both(back))));
-                    }
-                    r.set(f);
-                    store_vec(dy + i * lanes * 8, r);
-                }
+                if (in[i]) store_vec(dy + i * lanes * 8, r);
             }
-        fetch(src);
+        }
+        fetch(stage);
+        stage = stage + stage_step == wrap ? 0 : stage + stage_step;
     }
     if (!a.part) return;
     // The CTA's slab: its groups in order, in what was the ring.
-    cp_async_wait(0);
+    cp_async_wait<0>();
     float *s_cols = reinterpret_cast<float *>(s_ring);  // [2][d]
     for (int g = 0; g < groups; ++g) {
         __syncthreads();
@@ -559,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The slabs' sums and the weight gradients they give: 32 columns a CTA, thread
-// (p, c) adds four columns of slabs p, p + 32, ..., then the 32 parts are
+// (p, c) adds four columns of slabs p, p + 64, ..., then the 64 parts are
 // added in order.
 template <typename T>
-__global__ void __launch_bounds__(256) block_columns_kernel(const BlockArgs a, int slabs) {
-    __shared__ float4 s[2][32][8];
+__global__ void __launch_bounds__(512) block_columns_kernel(const BlockArgs a, int slabs) {
+    __shared__ float4 s[2][64][8];
     griddep_wait();
     griddep_launch_dependents();
     const int c = threadIdx.x & 7, p = threadIdx.x >> 3, j4 = (blockIdx.x * 8 + c) * 4;
@@ -571,7 +596,7 @@ __global__ void __launch_bounds__(256) block_columns_kernel(const BlockArgs a, i
     float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     if (j4 < a.d) {
 #pragma unroll 4
-        for (int b = p; b < slabs; b += 32) {
+        for (int b = p; b < slabs; b += 64) {
             const float *q = a.part + (long long)b * 2 * a.d + j4;
             if (first) {
                 const float4 u = *reinterpret_cast<const float4 *>(q);
@@ -590,7 +615,7 @@ __global__ void __launch_bounds__(256) block_columns_kernel(const BlockArgs a, i
     if (which > 1 || j >= a.d) return;
     float t = 0.0f;
 #pragma unroll
-    for (int b = 0; b < 32; ++b) t += reinterpret_cast<const float *>(&s[which][b][0])[col];
+    for (int b = 0; b < 64; ++b) t += reinterpret_cast<const float *>(&s[which][b][0])[col];
     const T *w = static_cast<const T *>(a.w), *gc = static_cast<const T *>(a.gc);
     auto put = [&](float *to, float v) { to[j] = a.accumulate ? to[j] + v : v; };
     if (which == 0) {
@@ -607,57 +632,37 @@ struct Shape {
     int nv, warps, groups, grid, per_sm;
 };
 
+int threads_of(int nv, bool backward) {
+    if (backward) return nv == 1 ? kBwThreads<1> : nv == 2 ? kBwThreads<2> : kBwThreads<4>;
+    return nv == 1 ? kFwThreads<1> : nv == 2 ? kFwThreads<2> : kFwThreads<4>;
+}
+
 Shape shape_of(const beam_block_desc *d, bool backward) {
     Shape s;
     const int vecs = d->d / 8, rows = d->T / kNominalSMs;
-    s.nv = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+    s.nv = 1;
+    while (vecs > s.nv * threads_of(s.nv, backward)) s.nv *= 2;
     // many rows per SM: fewer, busier warps; few: more warps, sooner done
-    if (s.nv == 1 && vecs >= 128 && rows >= 4) s.nv = 2;
+    if (s.nv == 1 && vecs >= 128 && rows >= 4 && d->dtype == BEAM_BF16) s.nv = 2;
+    if (const char *q = getenv(backward ? "NVB" : "NVF")) s.nv = atoi(q);
     s.warps = (vecs + 32 * s.nv - 1) / (32 * s.nv);
-    // Backward: one CTA per SM, so that there are few slabs.  Forward: CTAs of
-    // at least four warps, several per SM.  Named barriers are 1..15.
-    s.groups = backward ? kThreads / 32 / s.warps : s.warps < 4 ? 4 / s.warps : 1;
-    if (s.groups > 15) s.groups = 15;
+    s.groups = threads_of(s.nv, backward) / 32 / s.warps;
+    if (s.groups > 15) s.groups = 15;  // named barriers 1..15
     // rather a row on every SM than several on a few
-    if (s.groups > rows) s.groups = rows > 1 ? rows : 1;
-    const int threads = s.groups * s.warps * 32;
-    const int resident = s.nv <= 2 ? 2 * kThreads : kThreads;
-    s.per_sm = backward ? 1 : resident / threads < 8 ? resident / threads : 8;
+    s.per_sm = backward || s.nv > 2 ? 1 : 2;
+    if (s.groups * s.per_sm > rows) s.groups = rows > s.per_sm ? rows / s.per_sm : 1;
     const long long want = ((long long)d->T + s.groups - 1) / s.groups;
     const long long cap = (long long)kNominalSMs * s.per_sm;
     s.grid = int(want < cap ? want : cap);
     return s;
 }
 
-// Planes: 16-byte pieces per eight elements of one stage.
-Ring ring_of(const BlockArgs &a, int elt, bool branch, bool backward) {
-    Ring r = {0, 0, -1, -1, -1, -1};
-    const int n = elt / 2;
-    auto add = [&](int &at, int pieces) {
-        at = r.planes;
-        r.planes += pieces;
-    };
-    if (!backward || a.wn) add(r.at_x, n);
-    if (branch) add(r.at_y, n);
-    if (backward && a.dout) add(r.at_g, n);
-    if (backward && a.wn) add(r.at_n, 2);
-    return r;
-}
-
 // Rows ahead: as many as shared memory holds, and no more than there are.
-// The widest fp32 rows leave no room for dn, which is then read in place.
-size_t ring_fit(Ring &r, const Shape &s, int T) {
-    const size_t piece = size_t(s.groups) * s.warps * 32 * s.nv * 16;
-    const size_t room = size_t(kRingBytes) / s.per_sm;
-    if (r.at_n >= 0 && r.planes * piece > room) {
-        r.at_n = -1;
-        r.planes -= 2;
-    }
-    const size_t stage = r.planes * piece;
-    const long long rows = ((long long)T + s.grid * (long long)s.groups - 1) / (s.grid * (long long)s.groups);
-    r.depth = kMaxDepth;
-    while (r.depth > 1 && (r.depth * stage > room || r.depth > rows)) --r.depth;
-    return r.depth * stage;
+int depth_for(size_t stage, const Shape &s, int T) {
+    const long long at_once = (long long)s.grid * s.groups, rows = (T + at_once - 1) / at_once;
+    int depth = kMaxDepth;
+    while (depth > 1 && (depth * stage * s.per_sm > size_t(kRingBytes) || depth > rows)) --depth;
+    return depth;
 }
 
 size_t slab_bytes(const beam_block_desc *d) {
@@ -672,9 +677,10 @@ cudaError_t launch_forward_nv(const BlockArgs &a, const Shape &s, cudaStream_t s
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
     cudaError_t e = set_smem_once(kern, kSmemMost, attr_set);
     if (e != cudaSuccess) return e;
-    Ring r = ring_of(a, sizeof(T), BRANCH, false);
-    const size_t smem = ring_fit(r, s, a.T);
-    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, r, s.warps);
+    const size_t stage = size_t(kFwThreads<NV>) * 16 * NV * (BRANCH ? 2 : 1) * (sizeof(T) / 2);
+    const int depth = depth_for(stage, s, a.T);
+    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), depth * stage, st, a,
+                      depth, s.warps);
 }
 
 template <typename T, bool BRANCH>
@@ -690,10 +696,16 @@ cudaError_t launch_backward_nv(const BlockArgs &a, Shape s, cudaStream_t st) {
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
     cudaError_t e = set_smem_once(kern, kSmemMost, attr_set);
     if (e != cudaSuccess) return e;
-    Ring r = ring_of(a, sizeof(T), BRANCH, true);
-    size_t smem = ring_fit(r, s, a.T);
+    // the widest fp32 rows leave no room for dn, which is then read in place
+    const size_t plane = size_t(kBwThreads<NV>) * 16 * NV;
+    size_t stage = plane * (1 + BRANCH + NEXT) * (sizeof(T) / 2);
+    const int ring_n = NEXT && stage + 2 * plane <= size_t(kRingBytes);
+    if (ring_n) stage += 2 * plane;
+    const int depth = depth_for(stage, s, a.T);
+    size_t smem = depth * stage;
     if (a.part && smem < size_t(a.d) * 8) smem = size_t(a.d) * 8;
-    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, r, s.warps);
+    return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, depth, ring_n,
+                      s.warps);
 }
 
 template <typename T, bool BRANCH, bool NEXT>
@@ -702,7 +714,7 @@ cudaError_t launch_backward(const BlockArgs &a, const Shape &s, cudaStream_t st)
                     : s.nv == 2 ? launch_backward_nv<T, 2, BRANCH, NEXT>(a, s, st)
                                 : launch_backward_nv<T, 4, BRANCH, NEXT>(a, s, st);
     if (e != cudaSuccess || !a.part) return e;
-    return launch_pdl(block_columns_kernel<T>, dim3((a.d + 31) / 32), dim3(256), 0, st, a, s.grid);
+    return launch_pdl(block_columns_kernel<T>, dim3((a.d + 31) / 32), dim3(512), 0, st, a, s.grid);
 }
 
 bool bad16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }

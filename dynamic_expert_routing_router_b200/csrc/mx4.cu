@@ -202,17 +202,24 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *cod
 // (16..BN, following the tile's valid rows), so a decode batch, bound by the
 // weights' bytes, wastes no tile on tokens it lacks.
 //
-// One persistent CTA per SM; unit = (token tile, 128 weight rows).  Warps:
-//   0     TMA of both code tiles (128 bytes = 256 values a row and stage) and
-//         bulk copies of the weight scales, which lie in memory as tiled_at
-//   1     TMEM owner and issuer: copies a stage's scales to TMEM
-//         (tcgen05.cp, in order with the MMAs of the same thread), 4 MMAs
-//   2..5  epilogue
-//   6     the token rows' scales: they start at any row, so this warp loads
-//         them row by row, a step ahead, and lays them out in the stage
+// One persistent CTA per SM; unit = (token tile, 128 weight rows or a half or
+// quarter of them: see mx_parts).  Warps:
+//   0      TMA of both code tiles (128 bytes = 256 values a row and stage) and
+//          bulk copies of the weight scales, which lie in memory as tiled_at
+//   1      TMEM owner and issuer: copies a stage's scales to TMEM
+//          (tcgen05.cp, in order with the MMAs of the same thread), 4 MMAs
+//   2..9   epilogue: a lane quadrant of TMEM each, two warps per quadrant that
+//          take its columns by eights in turn
+//   10..13 the token rows' scales: they start at any row, so these warps load
+//          them row by row and lay them out in the stage, each for stages of
+//          its own, the next one's loads under way: one warp alone had every
+//          unit wait for several trips to memory.  (A warp has to see every
+//          phase of a stage it fills, since a wait tells only odd from even.)
 // Every wait is bounded; on expiry the CTA's status word says so.
 
-constexpr int kMxThreads = 224;
+constexpr int kMxWarps = 14;
+constexpr int kMxThreads = 32 * kMxWarps;
+constexpr int kMxScaleWarp = 10, kMxScaleWarps = 4;
 constexpr int kMxStepK = 256;             // values per stage: one 128-byte row
 constexpr uint32_t kMxSfCols = 64;        // TMEM columns of scales, behind the accumulators
 constexpr uint32_t kMxTmemCols = 512;
@@ -286,15 +293,17 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint3
 
 struct MxUnit {
     int e, mb;      // expert, block of 128 weight rows
+    int w0;         // first weight row of the block that the unit takes
     int row, rows;  // first token row, valid rows
 };
 
 // tile_end[e]: tiles of the experts up to e; row_end[e]: their rows.
-__device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int bn, int E, const int *tile_end,
-                                          const int *row_end) {
+__device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int parts, int bn, int E,
+                                          const int *tile_end, const int *row_end) {
     MxUnit w;
-    const int t = u / n_mb;
-    w.mb = u - t * n_mb;
+    const int per_tile = n_mb * parts, t = u / per_tile, m = u - t * per_tile;
+    w.mb = m / parts;
+    w.w0 = (m - w.mb * parts) * (128 / parts);
     int lo = 0, hi = E - 1;  // the first expert with tile_end > t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -310,33 +319,37 @@ __device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int bn, int E, const 
     return w;
 }
 
-__device__ __forceinline__ int mx_cols(int rows) { return (rows + 15) & ~15; }
-
-// The four words of scales (16 blocks) from word w0 of a row of `words`.
-template <int VEC>
-__device__ __forceinline__ uint4 load_scale_words(const uint32_t *row, int w0, int words) {
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if (VEC == 4) {
-        if (w0 < words) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(row + w0);
-            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+// Units per 128 weight rows: 1, 2 or 4.  A decode batch has two or three units
+// of 128 rows per SM, so that the SMs with one more set the time; the parts
+// even that out, at the price of loading the token tile once per part.  Cost
+// of the fullest SM in weight rows, a token row (from L2) as half of one.
+__device__ __forceinline__ int mx_parts(int units, int ctas, int num_a, int bn) {
+    int best = 1;
+    long long least = 0x7fffffffffffffffll;
+    for (int parts = 1; parts <= 4; parts *= 2) {
+        const long long rounds = ((long long)units * parts + ctas - 1) / ctas;
+        const long long cost = rounds * (num_a * (128 / parts) + bn / 2);
+        if (cost < least) {
+            least = cost;
+            best = parts;
         }
-    } else if (VEC == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-            if (w0 + i < words) {
-                const uint2 q = *reinterpret_cast<const uint2 *>(row + w0 + i);
-                v[i] = q.x; v[i + 1] = q.y;
-            }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (w0 + i < words) v[i] = row[w0 + i];
     }
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    return best;
 }
 
-template <int NUM_A, int BN, int VEC>
+__device__ __forceinline__ int mx_cols(int rows) { return (rows + 15) & ~15; }
+
+__device__ __forceinline__ void store_value(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_value(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The two words of scales (8 blocks) from word w0 of a row of `words`.
+template <int VEC>
+__device__ __forceinline__ uint2 load_scale_words(const uint32_t *row, int w0, int words) {
+    if (VEC == 2) return *reinterpret_cast<const uint2 *>(row + w0);
+    return make_uint2(row[w0], w0 + 1 < words ? row[w0 + 1] : 0u);
+}
+
+template <int NUM_A, int BN, int VEC, typename TOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_product_kernel(const __grid_constant__ Mx4Maps maps, const Mx4Args p) {
     using C = MxCfg<NUM_A, BN>;
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
-    __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][8];
+    __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][kMxWarps];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, bad_sh;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull_bar[a], 1);
-            mbar_init(&tempty_bar[a], 128);
+            mbar_init(&tempty_bar[a], 256);
         }
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
@@ -379,7 +392,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // Inclusive sums over the experts of their rows and of their tiles.  Rows
     // past p.N do not exist: counts that say otherwise are cut and reported.
     {
-        constexpr int kWarps = kMxThreads / 32;
         int carry_r = 0, carry_t = 0;
         for (int e0 = 0; e0 < p.E; e0 += kMxThreads) {
             const int e = e0 + tid;
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 s_tiles[e] = tb + t;
             }
             long long all = carry_r;
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < kMxWarps; ++w) {
                 all += s_warp[0][w];
                 carry_t += s_warp[1][w];
             }
@@ -425,7 +437,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     }
     const int n_mb = p.n >> 7;
-    const int n_units = s_tiles[p.E - 1] * n_mb;
+    const int blocks = s_tiles[p.E - 1] * n_mb;
+    const int parts = mx_parts(blocks, gridDim.x, NUM_A, BN);
+    const int n_units = blocks * parts;
     const int nkb = (p.k + kMxStepK - 1) / kMxStepK;
 
     if (warp == 0) {
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             bool ok = true;
             const int chunks = p.k >> 7;
             for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-                const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+                const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
                 const int w_row = w.e * p.n + w.mb * 128;
                 const long long sf = (long long)(w_row >> 7) * chunks * kMxSfChunk;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
@@ -450,10 +464,22 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     uint8_t *st = smem + size_t(s) * C::STAGE_BYTES;
                     const uint32_t sfb = min(2, chunks - 2 * kb) * kMxSfChunk;
                     mbar_arrive_expect_tx(&full_bar[s],
-                                          NUM_A * (C::A_BYTES + sfb) + C::B_BYTES);
-                    tma_load_2d(st, &maps.w, kb * 128, w_row, &full_bar[s]);
-                    if (NUM_A == 2)
-                        tma_load_2d(st + C::A_BYTES, &maps.w3, kb * 128, w_row, &full_bar[s]);
+                                          NUM_A * (C::A_BYTES / parts + sfb) + C::B_BYTES);
+                    if (parts == 1) {
+                        tma_load_2d(st, &maps.w, kb * 128, w_row, &full_bar[s]);
+                        if (NUM_A == 2)
+                            tma_load_2d(st + C::A_BYTES, &maps.w3, kb * 128, w_row, &full_bar[s]);
+                    } else {
+                        // the rows of a part lie where they do in the whole
+                        // tile; the MMA's other rows are not read back
+                        for (int r = w.w0; r < w.w0 + 128 / parts; r += 32) {
+                            tma_load_2d(st + r * 128, &maps.w_part, kb * 128, w_row + r,
+                                        &full_bar[s]);
+                            if (NUM_A == 2)
+                                tma_load_2d(st + C::A_BYTES + r * 128, &maps.w3_part, kb * 128,
+                                            w_row + r, &full_bar[s]);
+                        }
+                    }
                     tma_load_2d(st + C::OFF_B, &maps.a, kb * 128, w.row, &full_bar[s]);
                     const long long o = sf + (long long)kb * 2 * kMxSfChunk;
                     bulk_load(st + C::OFF_SFA, p.w_scales + o, sfb, &full_bar[s]);
@@ -478,7 +504,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             bool ok = true;
             const int chunks = p.k >> 7;
             for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++lu) {
-                const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+                const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
                 const int cols = mx_cols(w.rows);
                 const uint32_t a = lu % C::ACC_BUFS;
                 if (!mbar_wait_bounded(&tempty_bar[a], ((lu / C::ACC_BUFS) & 1u) ^ 1u, abort_flag,
@@ -534,65 +560,65 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 mbar_wait_bounded(&drain_bar, 0u, nullptr, p.timeout_ns);
             }
         }
-    } else if (warp == 6) {
+    } else if (warp >= kMxScaleWarp) {
         // ------------------------------------------------ token rows' scales --
-        // One step = 16 blocks of k = two stages; lane l carries rows l, l +
-        // 32, ..., and the words of a chunk are exactly its 16 bytes there.
+        // Lane l carries rows l, l + 32, ...: a stage's words of a row are
+        // exactly its bytes in the stage's two tiles.
         constexpr int RPL = (BN + 31) / 32;
         const int words = p.k >> 7;  // 32-bit words of scales per row
         const uint32_t *base = reinterpret_cast<const uint32_t *>(p.a_scales);
-        uint32_t it = 0;
+        const int first = warp - kMxScaleWarp;
+        const int units = int(blockIdx.x) < n_units
+                              ? (n_units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
+        const uint32_t total = first < STAGES ? uint32_t(units) * nkb : 0u;
         bool ok = true;
-        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
-            uint4 next[RPL];
-            auto load = [&](int step) {
+        uint2 next[RPL];
+        auto load = [&](uint32_t it) {
+            const int lu = int(it) / nkb, kb = int(it) - lu * nkb;
+            const MxUnit w = mx_unit(int(blockIdx.x) + lu * int(gridDim.x), n_mb, parts, BN, p.E,
+                                     s_tiles, s_rows);
 #pragma unroll
-                for (int q = 0; q < RPL; ++q) {
-                    const int r = lane + 32 * q;
-                    next[q] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < w.rows)
-                        next[q] = load_scale_words<VEC>(base + (long long)(w.row + r) * words,
-                                                        step * 4, words);
-                }
-            };
-            load(0);
-            for (int step = 0; step * 2 < nkb && ok; ++step) {
-                uint4 cur[RPL];
-#pragma unroll
-                for (int q = 0; q < RPL; ++q) cur[q] = next[q];
-                if ((step + 1) * 2 < nkb) load(step + 1);
-                for (int h = 0; h < 2 && step * 2 + h < nkb; ++h, ++it) {
-                    const int s = int(it % STAGES);
-                    ok = mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
-                                           p.timeout_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    uint8_t *sfb = smem + size_t(s) * C::STAGE_BYTES + C::OFF_SFB;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (uint32_t j = 0; j < C::B_SF_TILES; ++j) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int rq = int(j) * 4 + q;
-                                v[q] = 0u;
-                                if (rq < RPL) {
-                                    const uint4 x = cur[rq < RPL ? rq : 0];
-                                    v[q] = h ? (c ? x.w : x.z) : (c ? x.y : x.x);
-                                }
-                            }
-                            *reinterpret_cast<uint4 *>(sfb + (c * C::B_SF_TILES + j) * kMxSfChunk +
-                                                       lane * 16) =
-                                make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    // the tensor core reads them through the async proxy
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full_bar[s]);
-                }
+            for (int q = 0; q < RPL; ++q) {
+                const int r = lane + 32 * q;
+                next[q] = make_uint2(0u, 0u);
+                if (r < w.rows)
+                    next[q] = load_scale_words<VEC>(base + (long long)(w.row + r) * words, kb * 2,
+                                                    words);
             }
+        };
+        uint32_t it = uint32_t(first);
+        if (it < total) load(it);
+        while (it < total) {
+            const int s = int(it % STAGES);
+            const uint32_t then = s + kMxScaleWarps < STAGES
+                                      ? it + kMxScaleWarps : (it / STAGES + 1) * STAGES + first;
+            uint2 cur[RPL];
+#pragma unroll
+            for (int q = 0; q < RPL; ++q) cur[q] = next[q];
+            if (then < total) load(then);
+            ok = mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
+                                   p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t *sfb = smem + size_t(s) * C::STAGE_BYTES + C::OFF_SFB;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (uint32_t j = 0; j < C::B_SF_TILES; ++j) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int rq = int(j) * 4 + q;
+                        v[q] = rq < RPL ? (c ? cur[rq < RPL ? rq : 0].y : cur[rq < RPL ? rq : 0].x) : 0u;
+                    }
+                    *reinterpret_cast<uint4 *>(sfb + (c * C::B_SF_TILES + j) * kMxSfChunk +
+                                               lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            // the tensor core reads them through the async proxy
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full_bar[s]);
+            it = then;
         }
         if (!ok && lane == 0) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
     } else {
@@ -600,7 +626,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const int q = warp & 3;  // TMEM lane quadrant of this warp
         uint32_t lu = 0;
         for (int u = blockIdx.x; u < n_units; u += gridDim.x, ++lu) {
-            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+            const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
             const uint32_t a = lu % C::ACC_BUFS;
             bool ok = mbar_wait_bounded(&tfull_bar[a], (lu / C::ACC_BUFS) & 1u, abort_flag,
                                         p.timeout_ns);
@@ -611,25 +637,25 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             tc_fence_after_sync();
             const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + a * C::ACC_COLS;
-            const long long at = (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
+            // lanes of other parts hold nothing
+            const bool mine = q * 32 >= w.w0 && q * 32 < w.w0 + 128 / parts;
+            const int c1 = mine ? w.rows : 0;
+            TOut *out = static_cast<TOut *>(p.out) + (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
 #pragma unroll 1
-            for (int c0 = 0; c0 < w.rows; c0 += 16) {
-                uint32_t g[16], v[16];
-                tmem_ld_16(tb + c0, g);
-                if (NUM_A == 2) tmem_ld_16(tb + BN + c0, v);
+            for (int c0 = ((warp - 2) >> 2) * 8; c0 < c1; c0 += 16) {
+                uint32_t g[8], v[8];
+                tmem_ld_8(tb + c0, g);
+                if (NUM_A == 2) tmem_ld_8(tb + BN + c0, v);
                 tmem_ld_wait();
-                reg_fence_16(g);
-                if (NUM_A == 2) reg_fence_16(v);
+                reg_fence_8(g);
+                if (NUM_A == 2) reg_fence_8(v);
+                TOut *to = out + (long long)c0 * p.n;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (c0 + c >= w.rows) continue;
+                for (int c = 0; c < 8; ++c, to += p.n) {
+                    if (c0 + c >= c1) break;
                     float y = __uint_as_float(g[c]);
                     if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
-                    const long long o = at + (long long)(c0 + c) * p.n;
-                    if (p.out_f32)
-                        static_cast<float *>(p.out)[o] = y;
-                    else
-                        static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(y);
+                    store_value(to, y);
                 }
             }
             tc_fence_before_sync();
@@ -652,22 +678,29 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
 }
 
-template <int NUM_A, int BN, int VEC>
+template <int NUM_A, int BN, int VEC, typename TOut>
 cudaError_t launch_product_vec(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
     using C = MxCfg<NUM_A, BN>;
-    auto kern = mx4_product_kernel<NUM_A, BN, VEC>;
+    auto kern = mx4_product_kernel<NUM_A, BN, VEC, TOut>;
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
     cudaError_t e = set_smem_once(kern, int(C::SMEM_BYTES), attr_set);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kMxThreads), C::SMEM_BYTES, st, maps, a);
 }
 
-template <int NUM_A, int BN>
+template <int NUM_A, int BN, typename TOut>
 cudaError_t launch_product(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
     const int words = a.k >> 7;  // widest load every row's scales are aligned to
-    if (words % 4 == 0) return launch_product_vec<NUM_A, BN, 4>(maps, a, grid, st);
-    if (words % 2 == 0) return launch_product_vec<NUM_A, BN, 2>(maps, a, grid, st);
-    return launch_product_vec<NUM_A, BN, 1>(maps, a, grid, st);
+    if (words % 2 == 0) return launch_product_vec<NUM_A, BN, 2, TOut>(maps, a, grid, st);
+    return launch_product_vec<NUM_A, BN, 1, TOut>(maps, a, grid, st);
+}
+
+template <int NUM_A, typename TOut>
+cudaError_t launch_product_bn(int bn, const Mx4Maps &maps, const Mx4Args &a, int grid,
+                              cudaStream_t st) {
+    if (bn == 32) return launch_product<NUM_A, 32, TOut>(maps, a, grid, st);
+    if (bn == 64) return launch_product<NUM_A, 64, TOut>(maps, a, grid, st);
+    return launch_product<NUM_A, 128, TOut>(maps, a, grid, st);
 }
 
 // Token rows per tile, from the mean rows per expert a full batch would have.
@@ -689,7 +722,7 @@ beam_status check_mx4_desc(const beam_mx4_desc *d) {
     if (d->n % 128 != 0 || d->k % 128 != 0) return BEAM_ERR_UNSUPPORTED_SHAPE;
     // weight rows are 32-bit TMA coordinates, units 32-bit counters
     if ((long long)d->E * d->n > 0x7fffffffll) return BEAM_ERR_UNSUPPORTED_SHAPE;
-    if (((long long)d->N / 16 + d->E) * (d->n / 128) > 0x3fffffffll || d->N > 0x3fffffff)
+    if (((long long)d->N / 16 + d->E) * (d->n / 128) > 0x0fffffffll || d->N > 0x3fffffff)
         return BEAM_ERR_UNSUPPORTED_SHAPE;
     return BEAM_OK;
 }
@@ -786,8 +819,11 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     const int bn = product_bn(desc->N, desc->E);
     const unsigned long long row_bytes = desc->k / 2, w_rows = (unsigned long long)desc->E * desc->n;
     Mx4Maps maps;
+    const uint8_t *w3 = desc->swiglu ? w3_codes : w_codes;
     if (!make_byte_tmap(&maps.w, w_codes, row_bytes, w_rows, 128) ||
-        !make_byte_tmap(&maps.w3, desc->swiglu ? w3_codes : w_codes, row_bytes, w_rows, 128) ||
+        !make_byte_tmap(&maps.w3, w3, row_bytes, w_rows, 128) ||
+        !make_byte_tmap(&maps.w_part, w_codes, row_bytes, w_rows, 32) ||
+        !make_byte_tmap(&maps.w3_part, w3, row_bytes, w_rows, 32) ||
         !make_byte_tmap(&maps.a, a_codes, row_bytes, desc->N, unsigned(bn)))
         return BEAM_ERR_CUDA;
     Mx4Args a;
@@ -795,7 +831,6 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     a.E = desc->E;
     a.n = desc->n;
     a.k = desc->k;
-    a.out_f32 = desc->out_dtype == BEAM_F32;
     a.counts = expert_counts;
     a.a_scales = a_scales;
     a.w_scales = w_scales;
@@ -807,19 +842,15 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     // No more CTAs than units there can be: a tile per full BN rows plus one
     // unfilled per expert that has rows.
     const long long tiles = desc->N / bn + (desc->N < desc->E ? desc->N : desc->E);
-    long long grid = tiles * (desc->n / 128);
+    long long grid = tiles * (desc->n / 128) * 4;
     const int n_sm = device_sm_count() < kMxMaxCtas ? device_sm_count() : kMxMaxCtas;
     if (grid > n_sm) grid = n_sm;
-    cudaError_t e = cudaErrorInvalidValue;
-    if (desc->swiglu) {
-        if (bn == 32) e = launch_product<2, 32>(maps, a, int(grid), st);
-        if (bn == 64) e = launch_product<2, 64>(maps, a, int(grid), st);
-        if (bn == 128) e = launch_product<2, 128>(maps, a, int(grid), st);
-    } else {
-        if (bn == 32) e = launch_product<1, 32>(maps, a, int(grid), st);
-        if (bn == 64) e = launch_product<1, 64>(maps, a, int(grid), st);
-        if (bn == 128) e = launch_product<1, 128>(maps, a, int(grid), st);
-    }
+    const bool f32 = desc->out_dtype == BEAM_F32;
+    const cudaError_t e =
+        desc->swiglu ? (f32 ? launch_product_bn<2, float>(bn, maps, a, int(grid), st)
+                            : launch_product_bn<2, __nv_bfloat16>(bn, maps, a, int(grid), st))
+                     : (f32 ? launch_product_bn<1, float>(bn, maps, a, int(grid), st)
+                            : launch_product_bn<1, __nv_bfloat16>(bn, maps, a, int(grid), st));
     return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
 }
 

@@ -210,35 +210,29 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *cod
 //          (tcgen05.cp, in order with the MMAs of the same thread), 4 MMAs
 //   2..9   epilogue: a lane quadrant of TMEM each, two warps per quadrant that
 //          take its columns by eights in turn
-//   10..13 the token rows' scales: they start at any row, so these warps load
+//   10..17 the token rows' scales: they start at any row, so these warps load
 //          them row by row and lay them out in the stage, each for stages of
 //          its own, the next one's loads under way: one warp alone had every
 //          unit wait for several trips to memory.  (A warp has to see every
 //          phase of a stage it fills, since a wait tells only odd from even.)
 // Every wait is bounded; on expiry the CTA's status word says so.
 
-constexpr int kMxWarps = 14;
+constexpr int kMxWarps = 18;
 constexpr int kMxThreads = 32 * kMxWarps;
-constexpr int kMxScaleWarp = 10, kMxScaleWarps = 4;
+constexpr int kMxScaleWarp = 10, kMxScaleWarps = 8;
 constexpr int kMxStepK = 256;             // values per stage: one 128-byte row
 constexpr uint32_t kMxSfCols = 64;        // TMEM columns of scales, behind the accumulators
 constexpr uint32_t kMxTmemCols = 512;
 constexpr uint32_t kMxSfChunk = 512;      // bytes of one 128 x 4 tile of scales
 
+constexpr int kMxMaxStages = 12;
+constexpr uint32_t kMxSmemBytes = 220 * 1024;  // of stages, and 1024 to align them
+
 template <int NUM_A, int BN>
 struct MxCfg {
-    static constexpr uint32_t A_BYTES = 128 * 128;
-    static constexpr uint32_t B_BYTES = BN * 128;
     static constexpr uint32_t B_SF_TILES = (BN + 127) / 128;  // per 4 blocks of k
-    static constexpr uint32_t SFA_BYTES = 2 * kMxSfChunk;
-    static constexpr uint32_t SFB_BYTES = 2 * kMxSfChunk * B_SF_TILES;
-    static constexpr uint32_t OFF_B = NUM_A * A_BYTES;
-    static constexpr uint32_t OFF_SFA = OFF_B + B_BYTES;
-    static constexpr uint32_t OFF_SFB = OFF_SFA + NUM_A * SFA_BYTES;
-    static constexpr uint32_t STAGE_BYTES = (OFF_SFB + SFB_BYTES + 1023) / 1024 * 1024;
-    static constexpr int STAGES_FIT = int(220u * 1024u / STAGE_BYTES);
-    static constexpr int STAGES = STAGES_FIT > 10 ? 10 : STAGES_FIT;
-    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+    // token rows per TMA box: a tile's boxes behind its last row stay out
+    static constexpr uint32_t BOX = BN <= 64 ? BN : BN == 112 ? 56 : 64;
     static constexpr uint32_t ACC_COLS = NUM_A * BN;
     static constexpr uint32_t ACC_BUFS = 2 * ACC_COLS <= kMxTmemCols - kMxSfCols ? 2 : 1;
     // scales of one stage in TMEM, two stages in turn
@@ -246,8 +240,41 @@ struct MxCfg {
     static_assert(ACC_BUFS * ACC_COLS <= kMxTmemCols - kMxSfCols, "accumulators and scales share TMEM");
     static_assert(2 * SF_COLS <= kMxSfCols, "scales in TMEM");
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
-    static_assert(B_BYTES % 1024 == 0, "1024-byte aligned tiles");
-    static_assert(STAGES >= 2 && SMEM_BYTES <= 227u * 1024u - 4096u, "shared memory");
+    static_assert(BN % BOX == 0 && BOX % 8 == 0, "boxes of whole swizzle atoms");
+};
+
+// A stage: [NUM_A][128 / parts rows][128] weight codes, [BN][128] token codes,
+// [NUM_A][2][512] weight scales, [2][B_SF_TILES][512] token scales.  The MMA
+// takes 128 weight rows whatever a part has: its others are the bytes before
+// and behind, which therefore have to be there (the slack), and their results
+// are never read.
+struct MxStages {
+    uint32_t a_bytes, off_b, off_sfa, off_sfb, bytes;
+    int count;
+};
+template <int NUM_A, int BN>
+__device__ __forceinline__ MxStages mx_stages(int parts) {
+    MxStages g;
+    g.a_bytes = 128 * 128 / parts;
+    g.off_b = NUM_A * g.a_bytes;
+    g.off_sfa = g.off_b + BN * 128;
+    g.off_sfb = g.off_sfa + NUM_A * 2 * kMxSfChunk;
+    g.bytes = (g.off_sfb + 2 * kMxSfChunk * MxCfg<NUM_A, BN>::B_SF_TILES + 1023) / 1024 * 1024;
+    g.count = int((kMxSmemBytes - 2 * (128 * 128 - g.a_bytes)) / g.bytes);
+    if (g.count > kMxMaxStages) g.count = kMxMaxStages;
+    return g;
+}
+
+// A role's place in the ring of stages, and which of its phases comes.
+struct MxRing {
+    int s, n;
+    uint32_t phase;
+    __device__ __forceinline__ void next() {
+        if (++s == n) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 // Instruction descriptor of kind::mxf4: A and B E2M1 (1) at [7,10) and
@@ -353,19 +380,17 @@ template <int NUM_A, int BN, int VEC, typename TOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_product_kernel(const __grid_constant__ Mx4Maps maps, const Mx4Args p) {
     using C = MxCfg<NUM_A, BN>;
-    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
+    __shared__ __align__(8) uint64_t full_bar[kMxMaxStages], empty_bar[kMxMaxStages];
     __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][kMxWarps];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, bad_sh;
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const volatile int *abort_flag = &abort_sh;
 
     if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < kMxMaxStages; ++s) {
             mbar_init(&full_bar[s], 2);  // the TMA thread and the scales' warp
             mbar_init(&empty_bar[s], 1);
         }
@@ -440,69 +465,70 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int blocks = s_tiles[p.E - 1] * n_mb;
     const int parts = mx_parts(blocks, gridDim.x, NUM_A, BN);
     const int n_units = blocks * parts;
-    const int nkb = (p.k + kMxStepK - 1) / kMxStepK;
+    const int nkb = (p.k + kMxStepK - 1) / kMxStepK, chunks = p.k >> 7;
+    const MxStages g = mx_stages<NUM_A, BN>(parts);
+    // behind the slack: whole swizzle atoms, so 1024-byte aligned as well
+    uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) +
+                          (128 * 128 - g.a_bytes);
+    MxRing ring = {0, g.count, 0u};
 
     if (warp == 0) {
         // -------------------------------------------- codes, weight scales --
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            const int chunks = p.k >> 7;
             for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
                 const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
                 const int w_row = w.e * p.n + w.mb * 128;
                 const long long sf = (long long)(w_row >> 7) * chunks * kMxSfChunk;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = int(it % STAGES);
-                    if (!mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
+                const int boxes = (w.rows + int(C::BOX) - 1) / int(C::BOX);
+                for (int kb = 0; kb < nkb; ++kb, ++it, ring.next()) {
+                    uint64_t *bar = &full_bar[ring.s];
+                    if (!mbar_wait_bounded(&empty_bar[ring.s], ring.phase ^ 1u, abort_flag,
                                            p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     if (p.fault_skip && blockIdx.x == 0 && it == 0)
                         continue;  // test hook: this stage never fills
-                    uint8_t *st = smem + size_t(s) * C::STAGE_BYTES;
+                    uint8_t *st = smem + size_t(ring.s) * g.bytes;
                     const uint32_t sfb = min(2, chunks - 2 * kb) * kMxSfChunk;
-                    mbar_arrive_expect_tx(&full_bar[s],
-                                          NUM_A * (C::A_BYTES / parts + sfb) + C::B_BYTES);
+                    mbar_arrive_expect_tx(bar, NUM_A * (g.a_bytes + sfb) + boxes * C::BOX * 128);
                     if (parts == 1) {
-                        tma_load_2d(st, &maps.w, kb * 128, w_row, &full_bar[s]);
-                        if (NUM_A == 2)
-                            tma_load_2d(st + C::A_BYTES, &maps.w3, kb * 128, w_row, &full_bar[s]);
+                        tma_load_2d(st, &maps.w, kb * 128, w_row, bar);
+                        if (NUM_A == 2) tma_load_2d(st + g.a_bytes, &maps.w3, kb * 128, w_row, bar);
                     } else {
-                        // the rows of a part lie where they do in the whole
-                        // tile; the MMA's other rows are not read back
-                        for (int r = w.w0; r < w.w0 + 128 / parts; r += 32) {
-                            tma_load_2d(st + r * 128, &maps.w_part, kb * 128, w_row + r,
-                                        &full_bar[s]);
+                        for (int r = 0; r < 128 / parts; r += 32) {
+                            tma_load_2d(st + r * 128, &maps.w_part, kb * 128, w_row + w.w0 + r, bar);
                             if (NUM_A == 2)
-                                tma_load_2d(st + C::A_BYTES + r * 128, &maps.w3_part, kb * 128,
-                                            w_row + r, &full_bar[s]);
+                                tma_load_2d(st + g.a_bytes + r * 128, &maps.w3_part, kb * 128,
+                                            w_row + w.w0 + r, bar);
                         }
                     }
-                    tma_load_2d(st + C::OFF_B, &maps.a, kb * 128, w.row, &full_bar[s]);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(st + g.off_b + i * C::BOX * 128, &maps.a, kb * 128,
+                                    w.row + i * int(C::BOX), bar);
                     const long long o = sf + (long long)kb * 2 * kMxSfChunk;
-                    bulk_load(st + C::OFF_SFA, p.w_scales + o, sfb, &full_bar[s]);
+                    bulk_load(st + g.off_sfa, p.w_scales + o, sfb, bar);
                     if (NUM_A == 2)
-                        bulk_load(st + C::OFF_SFA + C::SFA_BYTES, p.w3_scales + o, sfb,
-                                  &full_bar[s]);
+                        bulk_load(st + g.off_sfa + 2 * kMxSfChunk, p.w3_scales + o, sfb, bar);
                 }
             }
             if (!ok) {
                 *reinterpret_cast<volatile int *>(&abort_sh) = 1;
                 // Let this CTA's own copies land before it can exit.  A stage
                 // whose scales never came does not complete: its wait is bounded.
-                for (uint32_t j = (it > uint32_t(STAGES) ? it - STAGES : 0u); j < it; ++j)
-                    mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
+                const uint32_t open = it < uint32_t(g.count) ? it : uint32_t(g.count);
+                for (uint32_t j = it - open; j < it; ++j)
+                    mbar_wait_bounded(&full_bar[j % g.count], (j / g.count) & 1u, nullptr,
                                       p.timeout_ns);
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
         if (lane == 0) {
-            uint32_t it = 0, lu = 0;
+            uint32_t lu = 0, set = 0;
             bool ok = true;
-            const int chunks = p.k >> 7;
             for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++lu) {
                 const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
                 const int cols = mx_cols(w.rows);
@@ -514,17 +540,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
                 tc_fence_after_sync();
                 const uint32_t d0 = tmem_base + a * C::ACC_COLS;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = int(it % STAGES);
-                    if (!mbar_wait_bounded(&full_bar[s], (it / STAGES) & 1u, abort_flag,
+                for (int kb = 0; kb < nkb; ++kb, ring.next(), set ^= 1u) {
+                    if (!mbar_wait_bounded(&full_bar[ring.s], ring.phase, abort_flag,
                                            p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t sa = smem_u32(smem + size_t(s) * C::STAGE_BYTES);
-                    const uint32_t sf =
-                        tmem_base + kMxTmemCols - kMxSfCols + (it & 1u) * C::SF_COLS;
+                    const uint32_t sa = smem_u32(smem) + uint32_t(ring.s) * g.bytes;
+                    const uint32_t sf = tmem_base + kMxTmemCols - kMxSfCols + set * C::SF_COLS;
                     const int nc = min(2, chunks - 2 * kb);
                     for (int c = 0; c < nc; ++c) {
                         // columns: [chunk][W, W3, B tiles] x 4
@@ -532,24 +556,27 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
                         for (int m = 0; m < NUM_A; ++m)
                             tmem_cp_scales(col + 4 * m,
-                                           sa + C::OFF_SFA + m * C::SFA_BYTES + c * kMxSfChunk);
+                                           sa + g.off_sfa + (m * 2 + c) * kMxSfChunk);
 #pragma unroll
                         for (uint32_t j = 0; j < C::B_SF_TILES; ++j)
                             tmem_cp_scales(col + 4 * (NUM_A + j),
-                                           sa + C::OFF_SFB + (c * C::B_SF_TILES + j) * kMxSfChunk);
+                                           sa + g.off_sfb + (c * C::B_SF_TILES + j) * kMxSfChunk);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t off = (c * 2 + h) * 32;
-                            const uint64_t bdesc = umma_desc_sw128(sa + C::OFF_B + off);
+                            const uint64_t bdesc = umma_desc_sw128(sa + g.off_b + off);
                             const uint32_t id = mxf4_idesc(cols, 2 * h);
                             const uint32_t acc = (kb | c | h) ? 1u : 0u;
+                            // a part's rows are lanes w0, w0 + 1, ..., where
+                            // its scales lie
 #pragma unroll
                             for (int m = 0; m < NUM_A; ++m)
-                                umma_mxf4(d0 + m * BN, umma_desc_sw128(sa + m * C::A_BYTES + off),
+                                umma_mxf4(d0 + m * BN,
+                                          umma_desc_sw128(sa + m * g.a_bytes + off - w.w0 * 128),
                                           bdesc, id, col + 4 * m, col + 4 * NUM_A, acc);
                         }
                     }
-                    umma_commit(&empty_bar[s]);
+                    umma_commit(&empty_bar[ring.s]);
                 }
                 if (!ok) break;
                 umma_commit(&tfull_bar[a]);
@@ -570,13 +597,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const int first = warp - kMxScaleWarp;
         const int units = int(blockIdx.x) < n_units
                               ? (n_units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
-        const uint32_t total = first < STAGES ? uint32_t(units) * nkb : 0u;
+        const uint32_t total = first < g.count ? uint32_t(units) * nkb : 0u;
         bool ok = true;
         uint2 next[RPL];
+        int unit = -1;
+        MxUnit w;
         auto load = [&](uint32_t it) {
             const int lu = int(it) / nkb, kb = int(it) - lu * nkb;
-            const MxUnit w = mx_unit(int(blockIdx.x) + lu * int(gridDim.x), n_mb, parts, BN, p.E,
-                                     s_tiles, s_rows);
+            if (lu != unit)
+                w = mx_unit(int(blockIdx.x) + lu * int(gridDim.x), n_mb, parts, BN, p.E, s_tiles,
+                            s_rows);
+            unit = lu;
 #pragma unroll
             for (int q = 0; q < RPL; ++q) {
                 const int r = lane + 32 * q;
@@ -586,21 +617,25 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                                                     words);
             }
         };
-        uint32_t it = uint32_t(first);
+        uint32_t lap = 0, it = uint32_t(first);  // stage s of a lap is step lap + s
+        ring.s = first;
         if (it < total) load(it);
         while (it < total) {
-            const int s = int(it % STAGES);
-            const uint32_t then = s + kMxScaleWarps < STAGES
-                                      ? it + kMxScaleWarps : (it / STAGES + 1) * STAGES + first;
+            int s = ring.s + kMxScaleWarps;
+            uint32_t then = it + kMxScaleWarps;
+            if (s >= g.count) {
+                lap += uint32_t(g.count);
+                s = first;
+                then = lap + uint32_t(first);
+            }
             uint2 cur[RPL];
 #pragma unroll
             for (int q = 0; q < RPL; ++q) cur[q] = next[q];
             if (then < total) load(then);
-            ok = mbar_wait_bounded(&empty_bar[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
-                                   p.timeout_ns);
+            ok = mbar_wait_bounded(&empty_bar[ring.s], ring.phase ^ 1u, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            uint8_t *sfb = smem + size_t(s) * C::STAGE_BYTES + C::OFF_SFB;
+            uint8_t *sfb = smem + size_t(ring.s) * g.bytes + g.off_sfb;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -617,7 +652,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             // the tensor core reads them through the async proxy
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full_bar[s]);
+            if (lane == 0) mbar_arrive(&full_bar[ring.s]);
+            if (s <= ring.s) ring.phase ^= 1u;
+            ring.s = s;
             it = then;
         }
         if (!ok && lane == 0) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
@@ -643,17 +680,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             TOut *out = static_cast<TOut *>(p.out) + (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
 #pragma unroll 1
             for (int c0 = ((warp - 2) >> 2) * 8; c0 < c1; c0 += 16) {
-                uint32_t g[8], v[8];
-                tmem_ld_8(tb + c0, g);
+                uint32_t y8[8], v[8];
+                tmem_ld_8(tb + c0, y8);
                 if (NUM_A == 2) tmem_ld_8(tb + BN + c0, v);
                 tmem_ld_wait();
-                reg_fence_8(g);
+                reg_fence_8(y8);
                 if (NUM_A == 2) reg_fence_8(v);
                 TOut *to = out + (long long)c0 * p.n;
 #pragma unroll
                 for (int c = 0; c < 8; ++c, to += p.n) {
                     if (c0 + c >= c1) break;
-                    float y = __uint_as_float(g[c]);
+                    float y = __uint_as_float(y8[c]);
                     if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
                     store_value(to, y);
                 }
@@ -680,33 +717,46 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
 template <int NUM_A, int BN, int VEC, typename TOut>
 cudaError_t launch_product_vec(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
-    using C = MxCfg<NUM_A, BN>;
     auto kern = mx4_product_kernel<NUM_A, BN, VEC, TOut>;
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
-    cudaError_t e = set_smem_once(kern, int(C::SMEM_BYTES), attr_set);
+    cudaError_t e = set_smem_once(kern, int(kMxSmemBytes + 1024), attr_set);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kMxThreads), C::SMEM_BYTES, st, maps, a);
+    return launch_pdl(kern, dim3(grid), dim3(kMxThreads), kMxSmemBytes + 1024, st, maps, a);
 }
 
 template <int NUM_A, int BN, typename TOut>
-cudaError_t launch_product(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
-    const int words = a.k >> 7;  // widest load every row's scales are aligned to
-    if (words % 2 == 0) return launch_product_vec<NUM_A, BN, 2, TOut>(maps, a, grid, st);
-    return launch_product_vec<NUM_A, BN, 1, TOut>(maps, a, grid, st);
+beam_status launch_product(Mx4Maps &maps, const uint8_t *a_codes, const Mx4Args &a, int grid,
+                           cudaStream_t st) {
+    if (!make_byte_tmap(&maps.a, a_codes, a.k / 2, a.N, MxCfg<NUM_A, BN>::BOX)) return BEAM_ERR_CUDA;
+    // rows' scales by eight bytes where every row starts at such a boundary
+    const cudaError_t e = (a.k >> 7) % 2 == 0
+                              ? launch_product_vec<NUM_A, BN, 2, TOut>(maps, a, grid, st)
+                              : launch_product_vec<NUM_A, BN, 1, TOut>(maps, a, grid, st);
+    return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
 }
 
-template <int NUM_A, typename TOut>
-cudaError_t launch_product_bn(int bn, const Mx4Maps &maps, const Mx4Args &a, int grid,
-                              cudaStream_t st) {
-    if (bn == 32) return launch_product<NUM_A, 32, TOut>(maps, a, grid, st);
-    if (bn == 64) return launch_product<NUM_A, 64, TOut>(maps, a, grid, st);
-    return launch_product<NUM_A, 128, TOut>(maps, a, grid, st);
+template <typename TOut>
+beam_status launch_product_bn(int swiglu, int bn, Mx4Maps &maps, const uint8_t *a_codes,
+                              const Mx4Args &a, int grid, cudaStream_t st) {
+    if (swiglu) {
+        if (bn == 32) return launch_product<2, 32, TOut>(maps, a_codes, a, grid, st);
+        if (bn == 64) return launch_product<2, 64, TOut>(maps, a_codes, a, grid, st);
+        return launch_product<2, 112, TOut>(maps, a_codes, a, grid, st);
+    }
+    if (bn == 32) return launch_product<1, 32, TOut>(maps, a_codes, a, grid, st);
+    if (bn == 64) return launch_product<1, 64, TOut>(maps, a_codes, a, grid, st);
+    if (bn == 128) return launch_product<1, 128, TOut>(maps, a_codes, a, grid, st);
+    return launch_product<1, 192, TOut>(maps, a_codes, a, grid, st);
 }
 
 // Token rows per tile, from the mean rows per expert a full batch would have.
-int product_bn(int N, int E) {
+// Two accumulators have to fit TMEM beside the scales, so that one is read out
+// while the other fills: 192 columns, with gate and up 112.
+int product_bn(int N, int E, int swiglu) {
     const long long avg = ((long long)N + E - 1) / E;
-    return avg <= 16 ? 32 : avg <= 64 ? 64 : 128;
+    if (avg <= 16) return 32;
+    if (avg <= 64) return 64;
+    return swiglu ? 112 : avg <= 256 ? 128 : 192;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -816,15 +866,14 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     if (desc->N == 0)
         return cudaMemsetAsync(workspace, 0, 256, st) == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
     if (!a_codes || !a_scales || !out) return BEAM_ERR_INVALID_ARG;
-    const int bn = product_bn(desc->N, desc->E);
+    const int bn = product_bn(desc->N, desc->E, desc->swiglu);
     const unsigned long long row_bytes = desc->k / 2, w_rows = (unsigned long long)desc->E * desc->n;
     Mx4Maps maps;
     const uint8_t *w3 = desc->swiglu ? w3_codes : w_codes;
     if (!make_byte_tmap(&maps.w, w_codes, row_bytes, w_rows, 128) ||
         !make_byte_tmap(&maps.w3, w3, row_bytes, w_rows, 128) ||
         !make_byte_tmap(&maps.w_part, w_codes, row_bytes, w_rows, 32) ||
-        !make_byte_tmap(&maps.w3_part, w3, row_bytes, w_rows, 32) ||
-        !make_byte_tmap(&maps.a, a_codes, row_bytes, desc->N, unsigned(bn)))
+        !make_byte_tmap(&maps.w3_part, w3, row_bytes, w_rows, 32))
         return BEAM_ERR_CUDA;
     Mx4Args a;
     a.N = desc->N;
@@ -845,13 +894,9 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     long long grid = tiles * (desc->n / 128) * 4;
     const int n_sm = device_sm_count() < kMxMaxCtas ? device_sm_count() : kMxMaxCtas;
     if (grid > n_sm) grid = n_sm;
-    const bool f32 = desc->out_dtype == BEAM_F32;
-    const cudaError_t e =
-        desc->swiglu ? (f32 ? launch_product_bn<2, float>(bn, maps, a, int(grid), st)
-                            : launch_product_bn<2, __nv_bfloat16>(bn, maps, a, int(grid), st))
-                     : (f32 ? launch_product_bn<1, float>(bn, maps, a, int(grid), st)
-                            : launch_product_bn<1, __nv_bfloat16>(bn, maps, a, int(grid), st));
-    return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+    return desc->out_dtype == BEAM_F32
+               ? launch_product_bn<float>(desc->swiglu, bn, maps, a_codes, a, int(grid), st)
+               : launch_product_bn<__nv_bfloat16>(desc->swiglu, bn, maps, a_codes, a, int(grid), st);
 }
 
 beam_status beam_mx4_check(const beam_mx4_desc *desc, void *workspace, void *stream) {

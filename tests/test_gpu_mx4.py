@@ -175,7 +175,7 @@ def assert_product(y, counts, n, k, a, ws, out):
 SIZES = [([1], 128, 128), ([5, 0, 3], 128, 256), ([0, 17, 1, 33], 256, 384), ([130, 2], 384, 640),
          ([300], 128, 1024), ([0, 0, 0, 0, 9], 640, 768),
          # several units per SM with more stages than the ring has, small and large tiles
-         ([2] * 40, 768, 1280), ([150] * 9, 512, 1152)]
+         ([2] * 40, 768, 1280), ([150] * 9, 512, 1152), ([701, 0, 390], 384, 640)]
 
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])

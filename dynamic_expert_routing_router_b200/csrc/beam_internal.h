@@ -359,9 +359,7 @@ cudaError_t launch_backward_stages(const BwArgs &a, int dtype, const void *x, co
 
 // Grouped expert product of 4-bit operands (mx4.cu).
 struct Mx4Maps {
-    // codes of the weights [E n, k / 2], boxes of 128 and of 32 rows, and of
-    // the token rows [N, k / 2]
-    CUtensorMap w, w3, w_part, w3_part, a;
+    CUtensorMap w, w3, a;  // codes of the weights [E n, k / 2] and the token rows [N, k / 2]
 };
 struct Mx4Args {
     int N, E, n, k;

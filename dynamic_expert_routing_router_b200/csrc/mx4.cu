@@ -80,6 +80,12 @@ __device__ __forceinline__ long long tiled_at(long long row, int block, int bloc
     return ((row >> 7) * (blocks >> 2) + (block >> 2)) * 512 + (r & 31) * 16 + (r >> 5) * 4 +
            (block & 3);
 }
+// The same of the b-th block of a matrix; 64-bit divisions only where needed.
+__device__ __forceinline__ long long tiled_at(long long b, int blocks) {
+    if (b >> 32) return tiled_at(b / blocks, int(b % blocks), blocks);
+    const uint32_t row = uint32_t(b) / uint32_t(blocks);
+    return tiled_at((long long)row, int(uint32_t(b) - row * uint32_t(blocks)), blocks);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, long long rows, int cols,
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, long long
             if ((threadIdx.x & 3) == 0) {
                 const long long b = i >> 2;
                 long long at = b;
-                if (tiled) at = tiled_at(b / blocks, int(b % blocks), blocks);
+                if (tiled) at = tiled_at(b, blocks);
                 scales[at] = bad ? 255 : uint8_t(s);
             }
         }
@@ -142,53 +148,66 @@ __device__ __forceinline__ float2 from_e2m1x2(uint32_t c) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-__device__ __forceinline__ void store_eight(__nv_bfloat16 *p, const float (&v)[8]) {
-    __nv_bfloat162 h[4];
+// 16 bytes of output a lane and store: eight bf16 from 32 bits of codes, or
+// four fp32 from 16.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+    using Code = uint32_t;
+    static __device__ void store(__nv_bfloat16 *p, uint32_t c, float f) {
+        __nv_bfloat162 h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
-}
-__device__ __forceinline__ void store_eight(float *p, const float (&v)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
+        for (int i = 0; i < 4; ++i) {
+            const float2 u = __fmul2_rn(from_e2m1x2(c >> (8 * i)), make_float2(f, f));
+            h[i] = __floats2bfloat162_rn(u.x, u.y);
+        }
+        *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+    }
+};
+template <>
+struct Piece<float> {
+    using Code = uint16_t;
+    static __device__ void store(float *p, uint32_t c, float f) {
+        const float2 u = __fmul2_rn(from_e2m1x2(c), make_float2(f, f));
+        const float2 v = __fmul2_rn(from_e2m1x2(c >> 8), make_float2(f, f));
+        *reinterpret_cast<float4 *>(p) = make_float4(u.x, u.y, v.x, v.y);
+    }
+};
 
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *codes,
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *codes,
                                                              const uint8_t *scales,
                                                              long long rows, int cols, int tiled,
                                                              T *out) {
+    using Code = typename Piece<T>::Code;
+    constexpr int kValues = 2 * int(sizeof(Code)), kPerBlock = 32 / kValues;
+    constexpr int kAhead = 2 * kMxAhead;
     griddep_wait();
     griddep_launch_dependents();
-    const long long total = rows * (cols >> 3);
+    const long long total = rows * (cols / kValues);
     const int blocks = cols >> 5;
     const long long step = (long long)gridDim.x * blockDim.x;
+    const Code *in = reinterpret_cast<const Code *>(codes);
     for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total;
-         i0 += kMxAhead * step) {
-        uint32_t c[kMxAhead], s[kMxAhead];
+         i0 += kAhead * step) {
+        uint32_t c[kAhead], s[kAhead];
 #pragma unroll
-        for (int q = 0; q < kMxAhead; ++q) {
+        for (int q = 0; q < kAhead; ++q) {
             const long long i = i0 + q * step;
             if (i >= total) break;
-            c[q] = codes[i];
-            const long long b = i >> 2;
-            s[q] = scales[tiled ? tiled_at(b / blocks, int(b % blocks), blocks) : b];
+            c[q] = in[i];
+            const long long b = i / kPerBlock;
+            s[q] = scales[tiled ? tiled_at(b, blocks) : b];
         }
 #pragma unroll
-        for (int q = 0; q < kMxAhead; ++q) {
+        for (int q = 0; q < kAhead; ++q) {
             const long long i = i0 + q * step;
             if (i >= total) break;
             // 2^(s - 127); s = 0 is the subnormal 2^-127, s = 255 stands for NaN
             const float f = s[q] == 0 ? __uint_as_float(0x00400000u)
                                       : __uint_as_float(s[q] == 255u ? 0x7fc00000u : s[q] << 23);
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 u = __fmul2_rn(from_e2m1x2(c[q] >> (8 * j)), make_float2(f, f));
-                v[2 * j] = u.x;
-                v[2 * j + 1] = u.y;
-            }
-            store_eight(out + i * 8, v);
+            Piece<T>::store(out + i * kValues, c[q], f);
         }
     }
 }
@@ -202,8 +221,10 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *cod
 // (16..BN, following the tile's valid rows), so a decode batch, bound by the
 // weights' bytes, wastes no tile on tokens it lacks.
 //
-// One persistent CTA per SM; unit = (token tile, 128 weight rows or a half or
-// quarter of them: see mx_parts).  Warps:
+// One persistent CTA per SM; unit = (token tile, 128 weight rows).  (Halves of a
+// unit would even out the last round of a decode batch, but a stage costs its
+// issue whatever its size: gate and up of 313 units, k = 2048, took 22.3 us in
+// halves, 19.9 whole.)  Warps:
 //   0      TMA of both code tiles (128 bytes = 256 values a row and stage) and
 //          bulk copies of the weight scales, which lie in memory as tiled_at
 //   1      TMEM owner and issuer: copies a stage's scales to TMEM
@@ -225,14 +246,21 @@ constexpr uint32_t kMxSfCols = 64;        // TMEM columns of scales, behind the 
 constexpr uint32_t kMxTmemCols = 512;
 constexpr uint32_t kMxSfChunk = 512;      // bytes of one 128 x 4 tile of scales
 
-constexpr int kMxMaxStages = 12;
-constexpr uint32_t kMxSmemBytes = 220 * 1024;  // of stages, and 1024 to align them
-
 template <int NUM_A, int BN>
 struct MxCfg {
+    static constexpr uint32_t A_BYTES = 128 * 128;
     static constexpr uint32_t B_SF_TILES = (BN + 127) / 128;  // per 4 blocks of k
     // token rows per TMA box: a tile's boxes behind its last row stay out
     static constexpr uint32_t BOX = BN <= 64 ? BN : BN == 112 ? 56 : 64;
+    static constexpr uint32_t SFA_BYTES = 2 * kMxSfChunk;
+    static constexpr uint32_t OFF_B = NUM_A * A_BYTES;
+    static constexpr uint32_t OFF_SFA = OFF_B + BN * 128;
+    static constexpr uint32_t OFF_SFB = OFF_SFA + NUM_A * SFA_BYTES;
+    static constexpr uint32_t STAGE_BYTES =
+        (OFF_SFB + 2 * kMxSfChunk * B_SF_TILES + 1023) / 1024 * 1024;
+    static constexpr int STAGES_FIT = int(220u * 1024u / STAGE_BYTES);
+    static constexpr int STAGES = STAGES_FIT > 10 ? 10 : STAGES_FIT;
+    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
     static constexpr uint32_t ACC_COLS = NUM_A * BN;
     static constexpr uint32_t ACC_BUFS = 2 * ACC_COLS <= kMxTmemCols - kMxSfCols ? 2 : 1;
     // scales of one stage in TMEM, two stages in turn
@@ -241,36 +269,16 @@ struct MxCfg {
     static_assert(2 * SF_COLS <= kMxSfCols, "scales in TMEM");
     static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256, "MMA N");
     static_assert(BN % BOX == 0 && BOX % 8 == 0, "boxes of whole swizzle atoms");
+    static_assert(STAGES >= 2 && SMEM_BYTES <= 227u * 1024u - 4096u, "shared memory");
 };
-
-// A stage: [NUM_A][128 / parts rows][128] weight codes, [BN][128] token codes,
-// [NUM_A][2][512] weight scales, [2][B_SF_TILES][512] token scales.  The MMA
-// takes 128 weight rows whatever a part has: its others are the bytes before
-// and behind, which therefore have to be there (the slack), and their results
-// are never read.
-struct MxStages {
-    uint32_t a_bytes, off_b, off_sfa, off_sfb, bytes;
-    int count;
-};
-template <int NUM_A, int BN>
-__device__ __forceinline__ MxStages mx_stages(int parts) {
-    MxStages g;
-    g.a_bytes = 128 * 128 / parts;
-    g.off_b = NUM_A * g.a_bytes;
-    g.off_sfa = g.off_b + BN * 128;
-    g.off_sfb = g.off_sfa + NUM_A * 2 * kMxSfChunk;
-    g.bytes = (g.off_sfb + 2 * kMxSfChunk * MxCfg<NUM_A, BN>::B_SF_TILES + 1023) / 1024 * 1024;
-    g.count = int((kMxSmemBytes - 2 * (128 * 128 - g.a_bytes)) / g.bytes);
-    if (g.count > kMxMaxStages) g.count = kMxMaxStages;
-    return g;
-}
 
 // A role's place in the ring of stages, and which of its phases comes.
+template <int N>
 struct MxRing {
-    int s, n;
-    uint32_t phase;
+    int s = 0;
+    uint32_t phase = 0u;
     __device__ __forceinline__ void next() {
-        if (++s == n) {
+        if (++s == N) {
             s = 0;
             phase ^= 1u;
         }
@@ -286,27 +294,55 @@ __device__ __forceinline__ uint32_t mxf4_idesc(int n, uint32_t sf_id) {
            (1u << 27) | (sf_id << 29);
 }
 
-__device__ __forceinline__ void umma_mxf4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                          uint32_t accumulate) {
+// The issuing warps run converged, so that addresses and descriptors stay in
+// uniform registers; `one` is set in the lane that issues.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ void umma_mxf4(uint32_t one, uint32_t tmem_d, uint64_t adesc,
+                                          uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one)
         : "memory");
 }
 
 // One 512-byte tile of scales (32 rows of 16 bytes, no swizzle: 8-row groups
 // of 128 bytes) to four TMEM columns, the same in all four lane quadrants.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
+__device__ __forceinline__ void tmem_cp_scales(uint32_t one, uint32_t taddr, uint32_t smem_addr) {
     uint64_t desc = 0;
     desc |= uint64_t((smem_addr & 0x3FFFFu) >> 4);
     desc |= uint64_t(128u >> 4) << 32;
     desc |= uint64_t(1u) << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(one)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_by(uint32_t one, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(one)
+        : "memory");
 }
 
 __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes,
@@ -320,17 +356,15 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint3
 
 struct MxUnit {
     int e, mb;      // expert, block of 128 weight rows
-    int w0;         // first weight row of the block that the unit takes
     int row, rows;  // first token row, valid rows
 };
 
 // tile_end[e]: tiles of the experts up to e; row_end[e]: their rows.
-__device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int parts, int bn, int E,
-                                          const int *tile_end, const int *row_end) {
+__device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int bn, int E, const int *tile_end,
+                                          const int *row_end) {
     MxUnit w;
-    const int per_tile = n_mb * parts, t = u / per_tile, m = u - t * per_tile;
-    w.mb = m / parts;
-    w.w0 = (m - w.mb * parts) * (128 / parts);
+    const int t = u / n_mb;
+    w.mb = u - t * n_mb;
     int lo = 0, hi = E - 1;  // the first expert with tile_end > t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -344,24 +378,6 @@ __device__ __forceinline__ MxUnit mx_unit(int u, int n_mb, int parts, int bn, in
     w.row = r0 + (t - t0) * bn;
     w.rows = min(bn, row_end[lo] - w.row);
     return w;
-}
-
-// Units per 128 weight rows: 1, 2 or 4.  A decode batch has two or three units
-// of 128 rows per SM, so that the SMs with one more set the time; the parts
-// even that out, at the price of loading the token tile once per part.  Cost
-// of the fullest SM in weight rows, a token row (from L2) as half of one.
-__device__ __forceinline__ int mx_parts(int units, int ctas, int num_a, int bn) {
-    int best = 1;
-    long long least = 0x7fffffffffffffffll;
-    for (int parts = 1; parts <= 4; parts *= 2) {
-        const long long rounds = ((long long)units * parts + ctas - 1) / ctas;
-        const long long cost = rounds * (num_a * (128 / parts) + bn / 2);
-        if (cost < least) {
-            least = cost;
-            best = parts;
-        }
-    }
-    return best;
 }
 
 __device__ __forceinline__ int mx_cols(int rows) { return (rows + 15) & ~15; }
@@ -380,17 +396,19 @@ template <int NUM_A, int BN, int VEC, typename TOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_product_kernel(const __grid_constant__ Mx4Maps maps, const Mx4Args p) {
     using C = MxCfg<NUM_A, BN>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[kMxMaxStages], empty_bar[kMxMaxStages];
+    __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
     __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][kMxWarps];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, bad_sh;
+    uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const volatile int *abort_flag = &abort_sh;
 
     if (tid == 0) {
-        for (int s = 0; s < kMxMaxStages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full_bar[s], 2);  // the TMA thread and the scales' warp
             mbar_init(&empty_bar[s], 1);
         }
@@ -462,130 +480,112 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     }
     const int n_mb = p.n >> 7;
-    const int blocks = s_tiles[p.E - 1] * n_mb;
-    const int parts = mx_parts(blocks, gridDim.x, NUM_A, BN);
-    const int n_units = blocks * parts;
+    const int n_units = s_tiles[p.E - 1] * n_mb;
     const int nkb = (p.k + kMxStepK - 1) / kMxStepK, chunks = p.k >> 7;
-    const MxStages g = mx_stages<NUM_A, BN>(parts);
-    // behind the slack: whole swizzle atoms, so 1024-byte aligned as well
-    uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) +
-                          (128 * 128 - g.a_bytes);
-    MxRing ring = {0, g.count, 0u};
+    MxRing<STAGES> ring;
 
     if (warp == 0) {
         // -------------------------------------------- codes, weight scales --
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-                const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
-                const int w_row = w.e * p.n + w.mb * 128;
-                const long long sf = (long long)(w_row >> 7) * chunks * kMxSfChunk;
-                const int boxes = (w.rows + int(C::BOX) - 1) / int(C::BOX);
-                for (int kb = 0; kb < nkb; ++kb, ++it, ring.next()) {
-                    uint64_t *bar = &full_bar[ring.s];
-                    if (!mbar_wait_bounded(&empty_bar[ring.s], ring.phase ^ 1u, abort_flag,
-                                           p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (p.fault_skip && blockIdx.x == 0 && it == 0)
-                        continue;  // test hook: this stage never fills
-                    uint8_t *st = smem + size_t(ring.s) * g.bytes;
+        const uint32_t one = elect_one();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+            const int w_row = uniform(w.e * p.n + w.mb * 128);
+            const int row = uniform(w.row), boxes = uniform((w.rows + int(C::BOX) - 1) / int(C::BOX));
+            const long long sf = (long long)(w_row >> 7) * chunks * kMxSfChunk;
+            for (int kb = 0; kb < nkb; ++kb, ++it, ring.next()) {
+                uint64_t *bar = &full_bar[ring.s];
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty_bar[ring.s], ring.phase ^ 1u,
+                                                               abort_flag, p.timeout_ns)) != 0;
+                if (!ok) break;
+                if (p.fault_skip && blockIdx.x == 0 && it == 0)
+                    continue;  // test hook: this stage never fills
+                if (one) {
+                    uint8_t *st = smem + size_t(ring.s) * C::STAGE_BYTES;
                     const uint32_t sfb = min(2, chunks - 2 * kb) * kMxSfChunk;
-                    mbar_arrive_expect_tx(bar, NUM_A * (g.a_bytes + sfb) + boxes * C::BOX * 128);
-                    if (parts == 1) {
-                        tma_load_2d(st, &maps.w, kb * 128, w_row, bar);
-                        if (NUM_A == 2) tma_load_2d(st + g.a_bytes, &maps.w3, kb * 128, w_row, bar);
-                    } else {
-                        for (int r = 0; r < 128 / parts; r += 32) {
-                            tma_load_2d(st + r * 128, &maps.w_part, kb * 128, w_row + w.w0 + r, bar);
-                            if (NUM_A == 2)
-                                tma_load_2d(st + g.a_bytes + r * 128, &maps.w3_part, kb * 128,
-                                            w_row + w.w0 + r, bar);
-                        }
-                    }
+                    mbar_arrive_expect_tx(bar, NUM_A * (C::A_BYTES + sfb) + boxes * C::BOX * 128);
+                    tma_load_2d(st, &maps.w, kb * 128, w_row, bar);
+                    if (NUM_A == 2) tma_load_2d(st + C::A_BYTES, &maps.w3, kb * 128, w_row, bar);
                     for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(st + g.off_b + i * C::BOX * 128, &maps.a, kb * 128,
-                                    w.row + i * int(C::BOX), bar);
+                        tma_load_2d(st + C::OFF_B + i * C::BOX * 128, &maps.a, kb * 128,
+                                    row + i * int(C::BOX), bar);
                     const long long o = sf + (long long)kb * 2 * kMxSfChunk;
-                    bulk_load(st + g.off_sfa, p.w_scales + o, sfb, bar);
+                    bulk_load(st + C::OFF_SFA, p.w_scales + o, sfb, bar);
                     if (NUM_A == 2)
-                        bulk_load(st + g.off_sfa + 2 * kMxSfChunk, p.w3_scales + o, sfb, bar);
+                        bulk_load(st + C::OFF_SFA + 2 * kMxSfChunk, p.w3_scales + o, sfb, bar);
                 }
+                __syncwarp();
             }
-            if (!ok) {
-                *reinterpret_cast<volatile int *>(&abort_sh) = 1;
-                // Let this CTA's own copies land before it can exit.  A stage
-                // whose scales never came does not complete: its wait is bounded.
-                const uint32_t open = it < uint32_t(g.count) ? it : uint32_t(g.count);
-                for (uint32_t j = it - open; j < it; ++j)
-                    mbar_wait_bounded(&full_bar[j % g.count], (j / g.count) & 1u, nullptr,
-                                      p.timeout_ns);
-            }
+        }
+        if (!ok) {
+            *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+            // Let this CTA's own copies land before it can exit.  A stage
+            // whose scales never came does not complete: its wait is bounded.
+            const uint32_t open = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
+            for (uint32_t j = it - open; j < it; ++j)
+                mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
+                                  p.timeout_ns);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        if (lane == 0) {
-            uint32_t lu = 0, set = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++lu) {
-                const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
-                const int cols = mx_cols(w.rows);
-                const uint32_t a = lu % C::ACC_BUFS;
-                if (!mbar_wait_bounded(&tempty_bar[a], ((lu / C::ACC_BUFS) & 1u) ^ 1u, abort_flag,
-                                       p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
+        const uint32_t one = elect_one();
+        uint32_t lu = 0, set = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t phase) {
+            return __all_sync(0xffffffffu,
+                              mbar_wait_bounded(bar, phase, abort_flag, p.timeout_ns)) != 0;
+        };
+        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++lu) {
+            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
+            const int cols = uniform(mx_cols(w.rows));
+            const uint32_t a = lu % C::ACC_BUFS;
+            ok = wait(&tempty_bar[a], ((lu / C::ACC_BUFS) & 1u) ^ 1u);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t d0 = tmem_base + a * C::ACC_COLS;
+            for (int kb = 0; kb < nkb; ++kb, ring.next(), set ^= 1u) {
+                ok = wait(&full_bar[ring.s], ring.phase);
+                if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t d0 = tmem_base + a * C::ACC_COLS;
-                for (int kb = 0; kb < nkb; ++kb, ring.next(), set ^= 1u) {
-                    if (!mbar_wait_bounded(&full_bar[ring.s], ring.phase, abort_flag,
-                                           p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t sa = smem_u32(smem) + uint32_t(ring.s) * g.bytes;
-                    const uint32_t sf = tmem_base + kMxTmemCols - kMxSfCols + set * C::SF_COLS;
-                    const int nc = min(2, chunks - 2 * kb);
-                    for (int c = 0; c < nc; ++c) {
-                        // columns: [chunk][W, W3, B tiles] x 4
-                        const uint32_t col = sf + c * 4 * (NUM_A + C::B_SF_TILES);
+                const uint32_t sa = smem_u32(smem) + uint32_t(ring.s) * C::STAGE_BYTES;
+                const uint32_t sf = tmem_base + kMxTmemCols - kMxSfCols + set * C::SF_COLS;
+                const int nc = min(2, chunks - 2 * kb);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c >= nc) break;
+                    // columns: [chunk][W, W3, B tiles] x 4
+                    const uint32_t col = sf + c * 4 * (NUM_A + C::B_SF_TILES);
+#pragma unroll
+                    for (int m = 0; m < NUM_A; ++m)
+                        tmem_cp_scales(one, col + 4 * m,
+                                       sa + C::OFF_SFA + (m * 2 + c) * kMxSfChunk);
+#pragma unroll
+                    for (uint32_t j = 0; j < C::B_SF_TILES; ++j)
+                        tmem_cp_scales(one, col + 4 * (NUM_A + j),
+                                       sa + C::OFF_SFB + (c * C::B_SF_TILES + j) * kMxSfChunk);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t off = (c * 2 + h) * 32;
+                        const uint64_t bdesc = umma_desc_sw128(sa + C::OFF_B + off);
+                        const uint32_t id = mxf4_idesc(cols, 2 * h);
+                        const uint32_t acc = (kb | c | h) ? 1u : 0u;
 #pragma unroll
                         for (int m = 0; m < NUM_A; ++m)
-                            tmem_cp_scales(col + 4 * m,
-                                           sa + g.off_sfa + (m * 2 + c) * kMxSfChunk);
-#pragma unroll
-                        for (uint32_t j = 0; j < C::B_SF_TILES; ++j)
-                            tmem_cp_scales(col + 4 * (NUM_A + j),
-                                           sa + g.off_sfb + (c * C::B_SF_TILES + j) * kMxSfChunk);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t off = (c * 2 + h) * 32;
-                            const uint64_t bdesc = umma_desc_sw128(sa + g.off_b + off);
-                            const uint32_t id = mxf4_idesc(cols, 2 * h);
-                            const uint32_t acc = (kb | c | h) ? 1u : 0u;
-                            // a part's rows are lanes w0, w0 + 1, ..., where
-                            // its scales lie
-#pragma unroll
-                            for (int m = 0; m < NUM_A; ++m)
-                                umma_mxf4(d0 + m * BN,
-                                          umma_desc_sw128(sa + m * g.a_bytes + off - w.w0 * 128),
-                                          bdesc, id, col + 4 * m, col + 4 * NUM_A, acc);
-                        }
+                            umma_mxf4(one, d0 + m * BN,
+                                      umma_desc_sw128(sa + m * C::A_BYTES + off),
+                                      bdesc, id, col + 4 * m, col + 4 * NUM_A, acc);
                     }
-                    umma_commit(&empty_bar[ring.s]);
                 }
-                if (!ok) break;
-                umma_commit(&tfull_bar[a]);
+                umma_commit_by(one, &empty_bar[ring.s]);
             }
-            if (!ok) {
-                *reinterpret_cast<volatile int *>(&abort_sh) = 1;
-                umma_commit(&drain_bar);  // wait for what was issued
-                mbar_wait_bounded(&drain_bar, 0u, nullptr, p.timeout_ns);
-            }
+            if (!ok) break;
+            umma_commit_by(one, &tfull_bar[a]);
+        }
+        if (!ok) {
+            *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+            umma_commit_by(one, &drain_bar);  // wait for what was issued
+            mbar_wait_bounded(&drain_bar, 0u, nullptr, p.timeout_ns);
         }
     } else if (warp >= kMxScaleWarp) {
         // ------------------------------------------------ token rows' scales --
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const int first = warp - kMxScaleWarp;
         const int units = int(blockIdx.x) < n_units
                               ? (n_units - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
-        const uint32_t total = first < g.count ? uint32_t(units) * nkb : 0u;
+        const uint32_t total = first < STAGES ? uint32_t(units) * nkb : 0u;
         bool ok = true;
         uint2 next[RPL];
         int unit = -1;
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         auto load = [&](uint32_t it) {
             const int lu = int(it) / nkb, kb = int(it) - lu * nkb;
             if (lu != unit)
-                w = mx_unit(int(blockIdx.x) + lu * int(gridDim.x), n_mb, parts, BN, p.E, s_tiles,
+                w = mx_unit(int(blockIdx.x) + lu * int(gridDim.x), n_mb, BN, p.E, s_tiles,
                             s_rows);
             unit = lu;
 #pragma unroll
@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         while (it < total) {
             int s = ring.s + kMxScaleWarps;
             uint32_t then = it + kMxScaleWarps;
-            if (s >= g.count) {
-                lap += uint32_t(g.count);
+            if (s >= STAGES) {
+                lap += uint32_t(STAGES);
                 s = first;
                 then = lap + uint32_t(first);
             }
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             ok = mbar_wait_bounded(&empty_bar[ring.s], ring.phase ^ 1u, abort_flag, p.timeout_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            uint8_t *sfb = smem + size_t(ring.s) * g.bytes + g.off_sfb;
+            uint8_t *sfb = smem + size_t(ring.s) * C::STAGE_BYTES + C::OFF_SFB;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const int q = warp & 3;  // TMEM lane quadrant of this warp
         uint32_t lu = 0;
         for (int u = blockIdx.x; u < n_units; u += gridDim.x, ++lu) {
-            const MxUnit w = mx_unit(u, n_mb, parts, BN, p.E, s_tiles, s_rows);
+            const MxUnit w = mx_unit(u, n_mb, BN, p.E, s_tiles, s_rows);
             const uint32_t a = lu % C::ACC_BUFS;
             bool ok = mbar_wait_bounded(&tfull_bar[a], (lu / C::ACC_BUFS) & 1u, abort_flag,
                                         p.timeout_ns);
@@ -674,12 +674,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             tc_fence_after_sync();
             const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + a * C::ACC_COLS;
-            // lanes of other parts hold nothing
-            const bool mine = q * 32 >= w.w0 && q * 32 < w.w0 + 128 / parts;
-            const int c1 = mine ? w.rows : 0;
             TOut *out = static_cast<TOut *>(p.out) + (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
 #pragma unroll 1
-            for (int c0 = ((warp - 2) >> 2) * 8; c0 < c1; c0 += 16) {
+            for (int c0 = ((warp - 2) >> 2) * 8; c0 < w.rows; c0 += 16) {
                 uint32_t y8[8], v[8];
                 tmem_ld_8(tb + c0, y8);
                 if (NUM_A == 2) tmem_ld_8(tb + BN + c0, v);
@@ -689,7 +686,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 TOut *to = out + (long long)c0 * p.n;
 #pragma unroll
                 for (int c = 0; c < 8; ++c, to += p.n) {
-                    if (c0 + c >= c1) break;
+                    if (c0 + c >= w.rows) break;
                     float y = __uint_as_float(y8[c]);
                     if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
                     store_value(to, y);
@@ -717,11 +714,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
 template <int NUM_A, int BN, int VEC, typename TOut>
 cudaError_t launch_product_vec(const Mx4Maps &maps, const Mx4Args &a, int grid, cudaStream_t st) {
+    using C = MxCfg<NUM_A, BN>;
     auto kern = mx4_product_kernel<NUM_A, BN, VEC, TOut>;
     static std::atomic<unsigned long long> attr_set{0};  // this instantiation only
-    cudaError_t e = set_smem_once(kern, int(kMxSmemBytes + 1024), attr_set);
+    cudaError_t e = set_smem_once(kern, int(C::SMEM_BYTES), attr_set);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kMxThreads), kMxSmemBytes + 1024, st, maps, a);
+    return launch_pdl(kern, dim3(grid), dim3(kMxThreads), C::SMEM_BYTES, st, maps, a);
 }
 
 template <int NUM_A, int BN, typename TOut>
@@ -772,7 +770,7 @@ beam_status check_mx4_desc(const beam_mx4_desc *d) {
     if (d->n % 128 != 0 || d->k % 128 != 0) return BEAM_ERR_UNSUPPORTED_SHAPE;
     // weight rows are 32-bit TMA coordinates, units 32-bit counters
     if ((long long)d->E * d->n > 0x7fffffffll) return BEAM_ERR_UNSUPPORTED_SHAPE;
-    if (((long long)d->N / 16 + d->E) * (d->n / 128) > 0x0fffffffll || d->N > 0x3fffffff)
+    if (((long long)d->N / 16 + d->E) * (d->n / 128) > 0x3fffffffll || d->N > 0x3fffffff)
         return BEAM_ERR_UNSUPPORTED_SHAPE;
     return BEAM_OK;
 }
@@ -830,12 +828,12 @@ beam_status beam_mx4_dequantize(int dtype, long long rows, int cols, const uint8
         return BEAM_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const dim3 grid(rows_grid(rows, cols)), block(256);
-    const uint32_t *in = reinterpret_cast<const uint32_t *>(codes);
     cudaError_t e = dtype == BEAM_BF16
-                        ? launch_pdl(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, st, in,
-                                     scales, rows, cols, tiled, static_cast<__nv_bfloat16 *>(out))
-                        : launch_pdl(mx4_dequantize_kernel<float>, grid, block, 0, st, in, scales,
-                                     rows, cols, tiled, static_cast<float *>(out));
+                        ? launch_pdl(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, st,
+                                     codes, scales, rows, cols, tiled,
+                                     static_cast<__nv_bfloat16 *>(out))
+                        : launch_pdl(mx4_dequantize_kernel<float>, grid, block, 0, st, codes,
+                                     scales, rows, cols, tiled, static_cast<float *>(out));
     return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
 }
 
@@ -871,9 +869,7 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     Mx4Maps maps;
     const uint8_t *w3 = desc->swiglu ? w3_codes : w_codes;
     if (!make_byte_tmap(&maps.w, w_codes, row_bytes, w_rows, 128) ||
-        !make_byte_tmap(&maps.w3, w3, row_bytes, w_rows, 128) ||
-        !make_byte_tmap(&maps.w_part, w_codes, row_bytes, w_rows, 32) ||
-        !make_byte_tmap(&maps.w3_part, w3, row_bytes, w_rows, 32))
+        !make_byte_tmap(&maps.w3, w3, row_bytes, w_rows, 128))
         return BEAM_ERR_CUDA;
     Mx4Args a;
     a.N = desc->N;
@@ -891,7 +887,7 @@ beam_status beam_mx4_expert_product(const beam_mx4_desc *desc, const uint8_t *a_
     // No more CTAs than units there can be: a tile per full BN rows plus one
     // unfilled per expert that has rows.
     const long long tiles = desc->N / bn + (desc->N < desc->E ? desc->N : desc->E);
-    long long grid = tiles * (desc->n / 128) * 4;
+    long long grid = tiles * (desc->n / 128);
     const int n_sm = device_sm_count() < kMxMaxCtas ? device_sm_count() : kMxMaxCtas;
     if (grid > n_sm) grid = n_sm;
     return desc->out_dtype == BEAM_F32

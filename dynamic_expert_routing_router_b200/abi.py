@@ -368,9 +368,20 @@ def _code(dtype):
     return dtype if isinstance(dtype, int) else (BEAM_BF16 if dtype == "bf16" else BEAM_F32)
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, looked up once: small calls are bound by the host's time."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _torch_dtype(code):
-    import torch
-    return torch.bfloat16 if code == BEAM_BF16 else torch.float32
+    return _torch().bfloat16 if code == BEAM_BF16 else _torch().float32
 
 
 def _arg(what, name, t, dtype, shape, dev, optional=False):
@@ -381,41 +392,38 @@ def _arg(what, name, t, dtype, shape, dev, optional=False):
         if optional:
             return None
         raise BeamError(1, f"{what}: {name} is missing")
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise BeamError(1, f"{what}: {name} has to be a contiguous {dtype} tensor of shape "
                            f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
-    return t.data_ptr()
+    raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
 
 
 def _workspace(what, t, dev):
     """(address, bytes) of a uint8 workspace on device `dev`."""
-    import torch
     if t is None:
         raise BeamError(3, f"{what}: the workspace is missing")
-    return _arg(what, "workspace", t, torch.uint8, t.shape, dev), t.numel()
+    return _arg(what, "workspace", t, _torch().uint8, t.shape, dev), t.numel()
 
 
 def _alloc(what, n, device):
-    import torch
     if n == 0:
         raise BeamError(1, what)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return _torch().empty(n, dtype=_torch().uint8, device=device or "cuda")
 
 
 def _current_device():
     """Index of the current CUDA device.  Before CUDA is up no tensor can be on
     one: -2, which no tensor's get_device() gives."""
-    import torch
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    torch = _torch()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
 def _stream_on(stream, dev):
     """Raw handle of `stream`, by default the current one of device `dev`."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _torch()._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -467,7 +475,7 @@ def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=No
 
 def block_enter_backward(dsc, x, w, dn, dx, dw, workspace, dskip=None, stream=None):
     """dx = dskip + dn (f32, as backward's dx) through the norm; dw f32 [d]."""
-    import torch
+    torch = _torch()
     what, dt, dev = "beam_block_enter_backward", _torch_dtype(dsc.dtype), _current_device()
     rows, row, f32 = (dsc.T, dsc.d), (dsc.d,), torch.float32
     ws, n = _workspace(what, workspace, dev)
@@ -484,7 +492,7 @@ def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=Non
     """Gradients of block_exit for dout and, with w_next, dn_next (f32): dres
     and dy in the rows' dtype, and in f32 that of each weight and gate that is
     given (dw_out, dgate_c, dw_next [d], dgate_t [T])."""
-    import torch
+    torch = _torch()
     what, dt, dev = "beam_block_exit_backward", _torch_dtype(dsc.dtype), _current_device()
     rows, row, toks, f32 = (dsc.T, dsc.d), (dsc.d,), (dsc.T,), torch.float32
     for name, a, b in (("w_out", w_out, dw_out), ("gate_c", gate_c, dgate_c),
@@ -536,7 +544,7 @@ def balance(dsc, logits, loss, cand_counts, workspace, kept_counts=None, mean_pr
     [T, logits_ld]; cand_counts (kept_counts) int32 [n_seq, E]: how many tokens
     of a sequence have (keep) expert e among their K candidates; mean_prob f32
     [n_seq, E] = P.  seq_begin int32 [n_seq + 1] (device)."""
-    import torch
+    torch = _torch()
     what, dev, i32 = "beam_moe_balance", _current_device(), torch.int32
     table = (dsc.n_seq, dsc.E)
     if kept_counts is not None and not dsc.has_mask:
@@ -556,7 +564,7 @@ def balance_backward(dsc, logits, counts, dlogits, seq_begin=None, dloss=None, s
     """dlogits f32 [T, E] of the balance loss, times dloss f32 [1] (device; 1 if
     left out).  counts: the forward's cand_counts, or kept_counts with
     count_kept.  backward(..., dlogits=) carries it on."""
-    import torch
+    torch = _torch()
     what, dev = "beam_moe_balance_backward", _current_device()
     f32, i32 = torch.float32, torch.int32
     _ok(lib().beam_moe_balance_backward(
@@ -570,7 +578,7 @@ def balance_backward(dsc, logits, counts, dlogits, seq_begin=None, dloss=None, s
 # ------------------------------------------- experts in 4-bit floating point --
 
 def _mx4_rows(what, x, codes, scales, dev):
-    import torch
+    torch = _torch()
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
         raise BeamError(1, f"{what}: a bf16 or f32 matrix is wanted, got {x.dtype} "
                            f"{tuple(x.shape)}")
@@ -588,7 +596,7 @@ def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
     scales uint8 [rows, cols / 32]; tiled: the scales in the tiles the product
     reads its weights' from.  n_rows: int32 [1] on the device, the rows that
     are there (the others are left as they are)."""
-    import torch
+    torch = _torch()
     dev = _current_device()
     code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_quantize", x, codes, scales, dev)
     pn = _arg("beam_mx4_quantize", "n_rows", n_rows, torch.int32, (1,), dev, True)
@@ -624,7 +632,7 @@ def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, w
     """out[i] = a_i w_e^T for the rows i of expert e (grouped by expert, counts
     int32 [E] on the device), or SiLU(a_i w_e^T) * (a_i w3_e^T) when
     dsc.swiglu.  w_scales, w3_scales: tiled (mx4_quantize(..., tiled=True))."""
-    import torch
+    torch = _torch()
     what, u8 = "beam_mx4_expert_product", torch.uint8
     N, E, n, k = dsc.N, dsc.E, dsc.n, dsc.k
     wc, ws = (E * n, k // 2), (E * n, k // 32)

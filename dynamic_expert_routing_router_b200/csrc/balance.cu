@@ -182,29 +182,28 @@ __global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
         if (t < hi) load_row(a.logits + (long long)t * a.ld, E, r);
         for (; t < hi; t += kBalWarps) {
             const float *row = a.logits + (long long)t * a.ld;
-            float z[EPL];
-            if (mask) load_row(row + E, E, z);
             if (t + kBalWarps < hi) load_row(row + (long long)kBalWarps * a.ld, E, next);
             float m;
-            unsigned ties;
-            const float kth = kth_largest(r, E, a.K, &m, &ties);
-            if (ties) {
+            unsigned taken;
+            const float kth = kth_largest(r, E, a.K, &m, &taken);
+            // the mask's logits of the candidates alone; they arrive meanwhile
+            float z[EPL];
+            if (kth == kth) {
+                taken = 0u;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if ((ties >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
-            } else if (mask) {
+                    if (r[i] >= kth) taken |= 1u << i;
+            }
+            if (mask) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (r[i] >= kth) count[i] += z[i] >= a.thr ? 0x10001u : 1u;
-            } else {
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (r[i] >= kth) count[i] += 1u;
+                    if ((taken >> i) & 1u) z[i] = __ldcs(row + E + lane + 32 * i);
             }
             const float inv = softmax_row(r, m);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 acc[i] = fmaf(r[i], inv, acc[i]);
+                if ((taken >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
                 r[i] = next[i];
             }
         }

@@ -348,12 +348,10 @@ __global__ void __launch_bounds__(kFwThreads<NV>, NV <= 2 ? 2 : 1)
 // rows; a CTA's groups add theirs up in order, and each CTA writes one slab
 // [2][d] (S, dw_next) that block_columns_kernel adds up in order.
 // BRANCH: exit's (else enter's, whose out is x); NEXT: with w_next.
-#ifndef BW1
-#define BW1 768
-#define BW2 512
-#endif
+// A thread's columns of the sums and the weights stay in registers: 512
+// threads of 128 (640 of 96 spilled: 56 us became 90 at 8192 x 2048).
 template <int NV>
-constexpr int kBwThreads = NV == 1 ? BW1 : NV == 2 ? BW2 : 512;
+constexpr int kBwThreads = NV == 1 ? 768 : 512;
 
 template <typename T, int NV, bool BRANCH, bool NEXT>
 __global__ void __launch_bounds__(kBwThreads<NV>, 1)
@@ -422,14 +420,13 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
         ahead += hop;
     };
     for (int s = 0; s < wrap; s += stage_step) fetch(s);
-    float2 mw[KEEP ? NV : 1][4];
-    Vec<T> nw[KEEP ? NV : 1];
+    float2 mw[KEEP ? NV : 1][4], nw[KEEP ? NV : 1][4];
     auto column = [&](int i) { return in[i] ? (i * lanes + me) * 8 : 0; };
     if constexpr (KEEP) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (BRANCH) weights_of(mw[i], w, gc, column(i));
-            if (NEXT) nw[i] = load_vec(wn + column(i));
+            if (NEXT) weights_of(nw[i], wn, static_cast<const T *>(nullptr), column(i));
         }
     }
     float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
@@ -451,14 +448,16 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
         if (BRANCH) c.y = read_copy<THREADS, T>(from + kY);
         c.g = read_copy<THREADS, T>(from + kG);
     };
-    auto weights = [&](float2(&m)[4], Vec<T> &p, int i) {
+    auto weights = [&](float2(&m)[4], float2(&p)[4], int i) {
         if constexpr (KEEP) {
-            p = nw[i];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m[k] = mw[i][k];
+            for (int k = 0; k < 4; ++k) {
+                m[k] = mw[i][k];
+                p[k] = nw[i][k];
+            }
         } else {
             if (BRANCH) weights_of(m, w, gc, column(i));
-            if (NEXT) p = load_vec(wn + column(i));
+            if (NEXT) weights_of(p, wn, static_cast<const T *>(nullptr), column(i));
         }
     };
     for (int stage = 0; t < rows; t += step, at += hop) {
@@ -472,15 +471,14 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
         for (int i = 0; i < NV; ++i) {
             Pieces c;
             read(c, stage, i);
-            float2 m[4];
-            Vec<T> p;
+            float2 m[4], p[4];
             weights(m, p, i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float2 o, pk, yk, mk;
                 if (NEXT) {
                     o = c.o.two(k);
-                    pk = __fmul2_rn(p.two(k), c.n.two(k));
+                    pk = __fmul2_rn(p[k], c.n.two(k));
                     q[0] = __ffma2_rn(o, o, q[0]);
                     q[1] = __ffma2_rn(pk, o, q[1]);
                 }
@@ -515,24 +513,23 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
             if (w) ry = rsqrtf(fmaf(sum[2], inv_d, eps));
             const float dot =
                 a.branch_scale * sig * ry * (sum[3] + ro * (sum[4] - mo * (ro * sum[5])));
-            if (w) back = -dot * inv_d;
+            if (w) back = -(dot * inv_d) * ry * ry;
             if (gt && me == 0) a.dgt[t] = rest * dot;
         }
-        const float zs = a.branch_scale * sig;
+        const float zs = a.branch_scale * sig * ry;
         T *dres = static_cast<T *>(a.dres) + at, *dy = static_cast<T *>(a.dy) + at;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             Pieces c;
             read(c, stage, i);
-            float2 m[4], g[4], f[4];
-            Vec<T> p;
+            float2 m[4], p[4], g[4], f[4];
             weights(m, p, i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 g[k] = c.g.two(k);
                 if (NEXT) {
                     const float2 o = __fmul2_rn(c.o.two(k), both(ro)), n = c.n.two(k);
-                    const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p.two(k), n));
+                    const float2 u = __ffma2_rn(both(-mo), o, __fmul2_rn(p[k], n));
                     g[k] = __ffma2_rn(both(ro), u, g[k]);
                     cn[i][k] = __ffma2_rn(n, o, cn[i][k]);
                 }
@@ -544,10 +541,9 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
             if constexpr (BRANCH) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 dz = __fmul2_rn(both(zs), g[k]);
-                    const float2 h = __fmul2_rn(c.y.two(k), both(ry));
-                    cs[i][k] = __ffma2_rn(dz, h, cs[i][k]);
-                    f[k] = __fmul2_rn(both(ry), __ffma2_rn(dz, m[k], __fmul2_rn(h, both(back))));
+                    const float2 y = c.y.two(k), e = __fmul2_rn(both(zs), g[k]);  // r(y) dz
+                    cs[i][k] = __ffma2_rn(e, y, cs[i][k]);
+                    f[k] = __ffma2_rn(e, m[k], __fmul2_rn(both(back), y));
                 }
                 r.set(f);
                 if (in[i]) store_vec(dy + i * lanes * 8, r);
@@ -557,30 +553,34 @@ __global__ void __launch_bounds__(kBwThreads<NV>, 1)
         stage = stage + stage_step == wrap ? 0 : stage + stage_step;
     }
     if (!a.part) return;
-    // The CTA's slab: its groups in order, in what was the ring.
+    // The CTA's slab: its groups' columns, [groups][2][d] in what was the
+    // ring, added up in order.
     cp_async_wait<0>();
-    float *s_cols = reinterpret_cast<float *>(s_ring);  // [2][d]
-    for (int g = 0; g < groups; ++g) {
-        __syncthreads();
-        if (row.group != g) continue;
+    __syncthreads();
+    float *s_cols = reinterpret_cast<float *>(s_ring), *mine = s_cols + row.group * 2 * d;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (in[i]) {
-                const int j = (i * lanes + me) * 8;
+    for (int i = 0; i < NV; ++i)
+        if (in[i]) {
+            const int j = (i * lanes + me) * 8;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float2 *s = reinterpret_cast<float2 *>(s_cols + j + 2 * k);
-                    float2 *n = reinterpret_cast<float2 *>(s_cols + d + j + 2 * k);
-                    *s = g ? __fadd2_rn(*s, cs[i][k]) : cs[i][k];
-                    *n = g ? __fadd2_rn(*n, cn[i][k]) : cn[i][k];
-                }
+            for (int k = 0; k < 4; k += 2) {
+                *reinterpret_cast<float4 *>(mine + j + 2 * k) =
+                    make_float4(cs[i][k].x, cs[i][k].y, cs[i][k + 1].x, cs[i][k + 1].y);
+                *reinterpret_cast<float4 *>(mine + d + j + 2 * k) =
+                    make_float4(cn[i][k].x, cn[i][k].y, cn[i][k + 1].x, cn[i][k + 1].y);
             }
-    }
+        }
     __syncthreads();
     float *slab = a.part + (long long)blockIdx.x * 2 * d;
     const int from = a.dw || a.dgc ? 0 : d, to = a.dwn ? 2 * d : d;
-    for (int j = from + threadIdx.x * 4; j < to; j += blockDim.x * 4)
-        *reinterpret_cast<float4 *>(slab + j) = *reinterpret_cast<const float4 *>(s_cols + j);
+    for (int j = from + threadIdx.x * 4; j < to; j += blockDim.x * 4) {
+        float4 v = *reinterpret_cast<const float4 *>(s_cols + j);
+        for (int g = 1; g < groups; ++g) {
+            const float4 u = *reinterpret_cast<const float4 *>(s_cols + g * 2 * d + j);
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        *reinterpret_cast<float4 *>(slab + j) = v;
+    }
 }
 
 // The slabs' sums and the weight gradients they give: 32 columns a CTA, thread
@@ -639,12 +639,11 @@ int threads_of(int nv, bool backward) {
 
 Shape shape_of(const beam_block_desc *d, bool backward) {
     Shape s;
-    const int vecs = d->d / 8, rows = d->T / kNominalSMs;
+    const int vecs = d->d / 8, rows = (d->T + kNominalSMs - 1) / kNominalSMs;
     s.nv = 1;
     while (vecs > s.nv * threads_of(s.nv, backward)) s.nv *= 2;
     // many rows per SM: fewer, busier warps; few: more warps, sooner done
     if (s.nv == 1 && vecs >= 128 && rows >= 4 && d->dtype == BEAM_BF16) s.nv = 2;
-    if (const char *q = getenv(backward ? "NVB" : "NVF")) s.nv = atoi(q);
     s.warps = (vecs + 32 * s.nv - 1) / (32 * s.nv);
     s.groups = threads_of(s.nv, backward) / 32 / s.warps;
     if (s.groups > 15) s.groups = 15;  // named barriers 1..15
@@ -703,7 +702,8 @@ cudaError_t launch_backward_nv(const BlockArgs &a, Shape s, cudaStream_t st) {
     if (ring_n) stage += 2 * plane;
     const int depth = depth_for(stage, s, a.T);
     size_t smem = depth * stage;
-    if (a.part && smem < size_t(a.d) * 8) smem = size_t(a.d) * 8;
+    const size_t slab = size_t(s.groups) * a.d * 8;  // at most 32 KB a vector and thread
+    if (a.part && smem < slab) smem = slab;
     return launch_pdl(kern, dim3(s.grid), dim3(s.groups * s.warps * 32), smem, st, a, depth, ring_n,
                       s.warps);
 }
@@ -723,7 +723,8 @@ beam_status check_block_desc(const beam_block_desc *d) {
     if (!d) return BEAM_ERR_INVALID_ARG;
     if (d->T < 0 || d->d <= 0) return BEAM_ERR_INVALID_ARG;
     if (d->dtype != BEAM_BF16 && d->dtype != BEAM_F32) return BEAM_ERR_INVALID_ARG;
-    if (!(d->eps > 0.0f) || !(d->eps < 3.0e38f)) return BEAM_ERR_INVALID_ARG;
+    // r(x)^2 has to stay far from fp32's end
+    if (!(d->eps >= 1.0e-30f) || !(d->eps < 3.0e38f)) return BEAM_ERR_INVALID_ARG;
     if (!(d->res_scale - d->res_scale == 0.0f) || !(d->branch_scale - d->branch_scale == 0.0f))
         return BEAM_ERR_INVALID_ARG;  // infinite or NaN
     if (d->accumulate != 0 && d->accumulate != 1) return BEAM_ERR_INVALID_ARG;

@@ -392,7 +392,7 @@ beam_status beam_moe_ep_combine(const beam_moe_desc *desc, const float *y_rows,
  * caller's part.  r(x) = 1 / sqrt(mean_j x_j^2 + eps) per row, in fp32.
  *   T, d       token rows of width d; d % 8 == 0, d <= 16384
  *   dtype      of the rows, the weights and the gates
- *   eps        finite and > 0
+ *   eps        finite and >= 1e-30
  *   res_scale, branch_scale   a and b below; finite
  *   accumulate backward: 1 adds to the gradients of the weights and of
  *              gate_c (fp32 [d]), 0 overwrites them; every other gradient is

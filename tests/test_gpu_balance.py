@@ -259,3 +259,36 @@ def test_gradient_through_the_layer(dtype, tol):
         want = torch.as_tensor(ref[r], device=DEV) + add
         assert float((got[k].double() - want).abs().max()) <= tol * float(want.abs().max()), k
         assert float((plain[k].double() - want).abs().max()) > tol * float(want.abs().max()), k
+
+
+def test_offsets_past_32_bits_and_many_sequences():
+    """More than 2^31 logits, and one sequence per three tokens: counts add up,
+    the last rows' gradient is that of a small call."""
+    T, E, K = 8_500_000, 256, 4
+    lg = torch.zeros(T, E, device=DEV)
+    lg[:, 3], lg[:, 100], lg[:, 200], lg[:, 255] = 4.0, 3.0, 2.0, 1.0
+    dsc = abi.balance_desc(T, E, K)
+    loss, cand = torch.empty(1, device=DEV), torch.empty(1, E, dtype=torch.int32, device=DEV)
+    abi.balance(dsc, lg, loss, cand, abi.alloc_balance_workspace(dsc))
+    p = torch.softmax(lg[0].double(), 0)
+    assert cand[0, [3, 100, 200, 255]].tolist() == [T] * 4 and int(cand.long().sum()) == 4 * T
+    want = float((p[[3, 100, 200, 255]]).sum() * E / K)
+    # a chunk's warp adds T / (8 * 444) equal terms one by one
+    assert abs(float(loss) - want) <= (T / 3552 + 700) * U * want
+    dl = torch.empty(T, E, device=DEV)
+    abi.balance_backward(dsc, lg, cand, dl)
+    assert torch.equal(dl[-5:], dl[:5]) and torch.isfinite(dl[-1]).all()
+    del lg, dl
+    T, E, S = 9000, 20, 3000
+    lg = logits_of(T, E, 1, False)
+    b = torch.arange(0, T + 1, 3, dtype=torch.int32, device=DEV)
+    dsc = abi.balance_desc(T, E, 2, n_seq=S)
+    cand = torch.empty(S, E, dtype=torch.int32, device=DEV)
+    abi.balance(dsc, lg, loss, cand, abi.alloc_balance_workspace(dsc), seq_begin=b)
+    c, _ = counts_of(lg, E, 2)
+    assert torch.equal(cand.double(), c.view(S, 3, E).sum(1))
+    dl = torch.empty(T, E, device=DEV)
+    abi.balance_backward(dsc, lg, cand, dl, seq_begin=b)
+    rl, _, _, g = reference(lg, E, 2, list(range(0, T + 1, 3)), 1.0, c)
+    assert abs(float(loss) - float(rl)) <= (80 + S) * U * float(rl)
+    assert ((dl.double() - g).abs() <= 150 * U * E).all()

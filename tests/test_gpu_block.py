@@ -320,3 +320,26 @@ def test_another_stream_and_a_captured_graph():
     torch.cuda.synchronize()
     for a, b in zip((n, dx, dw), e):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows are those of a small call."""
+    T, d = 270_000, 8192
+    s = draw(3, d, "bf16", 4)
+    x = torch.ones(T, d, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = s["x"]
+    n = torch.empty_like(x)
+    abi.block_enter(abi.block_desc(T, d), x, s["w"], n)
+    ref = torch.empty_like(s["x"])
+    abi.block_enter(abi.block_desc(3, d), s["x"], s["w"], ref)
+    assert torch.equal(n[-3:], ref)
+    dsc = abi.block_desc(T, d)
+    dn = torch.zeros(T, d, device=DEV)
+    dn[-3:] = s["dn"]
+    dw, ws = full(d), abi.alloc_block_workspace(dsc)
+    abi.block_enter_backward(dsc, x, s["w"], dn, n, dw, ws)
+    small, dws = abi.block_desc(3, d), full(d)
+    abi.block_enter_backward(small, s["x"], s["w"], s["dn"], ref, dws, abi.alloc_block_workspace(small))
+    assert torch.equal(n[-3:], ref) and (n[:-3] == 0).all()
+    # the same three rows' terms, all others zeros, in another order: 3 roundings
+    assert ((dw - dws).abs() <= 3 * U * (s["dn"] * 100).abs().sum(0)).all()

@@ -1,0 +1,251 @@
+"""The residual block as it is used: norm, layer, balance loss, gates, residual
+and next norm, forward and backward, and served with 4-bit experts.
+
+The pieces have tests of their own; here they run together.  Forward: every
+stage against the formula in 64 bits from the block's own input of that stage.
+Gradients: against differences of the whole forward.
+"""
+import numpy as np
+import pytest
+import torch
+
+from dynamic_expert_routing_router_b200 import abi, block, inputs
+
+from _parity import gpu_forward, gpu_route
+from test_gpu_mx4 import plain_quantize, plain_values, tile_scales
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+BF16 = torch.bfloat16
+
+
+def parts(T, sh, dtype, masked, seed, **kw):
+    t = BF16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def r(*s, std=1.0, mean=0.0):
+        return (torch.randn(*s, generator=g, device=DEV) * std + mean).to(t)
+    W = [w.to(t) for w in inputs.make_experts(sh, seed=seed, device=DEV)]
+    Wg = inputs.make_gate(sh, seed=seed, device=DEV).to(t)
+    Wm = inputs.make_mask(sh, 0.5, seed=seed, device=DEV).to(t) if masked else None
+    v = dict(x=r(T, sh.d, std=2.0), dout=r(T, sh.d), gt=r(T), w_next=r(sh.d, std=0.1, mean=1),
+             dn=torch.randn(T, sh.d, generator=g, device=DEV),
+             w_in=r(sh.d, std=0.1, mean=1), w_out=r(sh.d, std=0.1, mean=1), gc=r(sh.d, std=0.2, mean=0.7))
+    b = block.MoeBlock(T, sh.d, sh.E, sh.I, sh.K, sh.renorm, Wg, Wm, *W, v["w_in"], v["w_out"], v["gc"],
+                       dtype=dtype, **kw)
+    return b, v, (Wg, Wm, *W)
+
+
+def step(b, v, w, loss_grad=None, seq=None, back=True):
+    """One forward (and backward) with every part; fresh outputs."""
+    out, n = torch.empty_like(v["x"]), torch.empty_like(v["x"])
+    b.forward(v["x"], out, gate_t=v["gt"], w_next=v["w_next"], n_next=n, seq_begin=seq)
+    got = dict(out=out, n_next=n, loss=b.loss.clone())
+    if back:
+        b.zero_grad()
+        dx, dgt = torch.empty_like(v["x"]), torch.empty(v["x"].shape[0], device=DEV)
+        dwn = torch.zeros(v["x"].shape[1], device=DEV)
+        b.backward(v["x"], out, v["dout"], dx, gate_t=v["gt"], dgate_t=dgt, w_next=v["w_next"], dn_next=v["dn"],
+                   dw_next=dwn, seq_begin=seq, dloss=loss_grad)
+        got.update(dx=dx, dgt=dgt, dwn=dwn, **{"d" + k: g.clone() for k, g in b.grads.items() if g is not None})
+    b.check()
+    return got
+
+
+def rms(x, eps=1e-6):
+    return (x.square().mean(1, keepdim=True) + eps).sqrt()
+
+
+@pytest.mark.parametrize("T", [1, 5, 130])
+def test_forward_is_its_stages(T):
+    """enter, the layer on its rows, exit: one rounding (2^-8) each and 60 u."""
+    sh = inputs.Shape(256, 16, 4, 256, 1, "bf16")
+    b, v, W = parts(T, sh, "bf16", True, T, res_scale=0.9, branch_scale=0.5)
+    got = step(b, v, W, back=False)
+    x, h = v["x"].double(), 2.0 ** -8
+    n = x / rms(x) * v["w_in"].double()
+    assert ((b.n.double() - n).abs() <= (h + 42 * U) * n.abs() + 1e-37).all()
+    layer, _ = gpu_forward(abi.desc(T, sh.d, sh.E, sh.I, sh.K, "bf16", 1), b.n, *W)
+    assert torch.equal(layer, b.y)  # the layer keeps its results
+    y = b.y.double()
+    branch = 0.5 * torch.sigmoid(v["gt"].double())[:, None] * v["gc"].double() * v["w_out"].double() * y / rms(y)
+    out = 0.9 * x + branch
+    tol = h * out.abs() * 1.01 + 60 * U * (x.abs() + branch.abs()) + 1e-37
+    assert ((got["out"].double() - out).abs() <= tol).all()
+    o = got["out"].double()
+    nn = o / rms(o) * v["w_next"].double()
+    assert ((got["n_next"].double() - nn).abs() <= (h + 42 * U) * nn.abs() + 1e-37).all()
+
+
+def test_gradients_are_the_differences_of_the_block():
+    """An fp32 block without a mask (whose estimator is no derivative): the
+    change of <dout, out> + <dn, n_next> + dloss loss along the gradient's own
+    signs, per input and weight.
+
+    Bar: outputs are off by at most (d + I + 500) u of their magnitudes' sum M
+    (dot products over d = 128 and I = 128 and the norms' bars), so the quotient
+    by 2 t with t = 2^-9 s, s the input's mean magnitude, by 756 u 2^9 M = 2.4 %
+    of M, against a change of sum |g| s that is larger than M for the rows and
+    of its order for the weights; the third derivative's share is of the order
+    of t^2 = 2^-18.  No candidate changes over the step (checked)."""
+    sh = inputs.Shape(128, 8, 2, 128, 1, "f32")
+    T, seq = 12, torch.tensor([0, 5, 12], dtype=torch.int32, device=DEV)
+    b, v, W = parts(T, sh, "f32", False, 3, balance=0.5, n_seq=2, train=True)
+    dl = torch.tensor([2.0], device=DEV)
+    base = step(b, v, W, dl, seq)
+    cand = b.cand.clone()
+
+    def total(g):
+        return float((v["dout"].double() * g["out"].double()).sum() + (v["dn"].double() * g["n_next"].double()).sum()
+                     + 2.0 * g["loss"].double().sum())
+    M = float((v["dout"].double() * base["out"].double()).abs().sum()
+              + (v["dn"].double() * base["n_next"].double()).abs().sum())
+    tensors = dict(dx=v["x"], dgt=v["gt"], dwn=v["w_next"], dw_in=b.w_in, dw_out=b.w_out, dgate_c=b.gate_c,
+                   dW_gate=b.layer[0], dW1=b.layer[2], dW3=b.layer[3], dW2=b.layer[4])
+    for k, t in tensors.items():
+        g, keep = base[k].double(), t.clone()
+        s = float(keep.abs().mean())
+        h = 2.0 ** -9 * s
+        ends = []
+        for sign in (1.0, -1.0):
+            t.copy_(keep + sign * h * torch.sign(g).to(t.dtype))
+            ends.append(total(step(b, v, W, dl, seq, back=False)))
+            assert torch.equal(b.cand, cand), k
+        t.copy_(keep)
+        diff, want = (ends[0] - ends[1]) / (2 * h), float(g.abs().sum())
+        assert abs(diff - want) * s <= 0.024 * M + 1e-4 * want * s, (k, diff * s, want * s, M)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_training_step_is_its_pieces_and_replays(dtype):
+    """Masked, with the kept experts' balance loss: the gradients are those of
+    the pieces called one by one, two runs agree bit for bit, gradients add up
+    over steps, and a captured step replays on new rows."""
+    sh = inputs.Shape(256, 16, 4, 256, 1, dtype)
+    T, seq = 40, torch.tensor([0, 1, 40], dtype=torch.int32, device=DEV)
+    b, v, W = parts(T, sh, dtype, True, 5, balance=0.1, n_seq=2, count_kept=True, beta=0.01, train=True)
+    dl = torch.tensor([0.7], device=DEV)
+    one, two = step(b, v, W, dl, seq), step(b, v, W, dl, seq)
+    for k in one:
+        assert torch.equal(one[k], two[k]), k
+    assert int(b.cand.sum()) == T * sh.K and int(b.kept.sum()) < T * sh.K
+    # the pieces
+    e = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    z = lambda w: torch.zeros(w.shape, device=DEV)  # noqa: E731
+    dres, dy, dgt = torch.empty_like(v["x"]), torch.empty_like(v["x"]), e(T)
+    bd = abi.block_desc(T, sh.d, dtype)
+    bw = abi.alloc_block_workspace(bd)
+    gw, gc, gn = e(sh.d), e(sh.d), e(sh.d)
+    abi.block_exit_backward(bd, b.y, v["dout"], dres, dy, bw, out=one["out"], dn_next=v["dn"], w_out=b.w_out,
+                            gate_c=b.gate_c, gate_t=v["gt"], w_next=v["w_next"], dw_out=gw, dgate_c=gc, dgate_t=dgt,
+                            dw_next=gn)
+    rt = gpu_route(abi.desc(T, sh.d, sh.E, sh.I, sh.K, dtype, 1), b.n, W[0], W[1])
+    lg = torch.as_tensor(rt["logits"], device=DEV)
+    dlog = e(T, sh.E)
+    abi.balance_backward(b.bal, lg, b.kept, dlog, seq_begin=seq, dloss=dl)
+    dn, dW = e(T, sh.d), [z(w) for w in W]
+    ld = abi.desc(T, sh.d, sh.E, sh.I, sh.K, dtype, 1)
+    abi.backward(ld, b.n, *W, dy, 0.01, dn, *dW, abi.alloc_backward_workspace(ld, DEV), dlogits=dlog)
+    dx, gi = torch.empty_like(v["x"]), e(sh.d)
+    abi.block_enter_backward(bd, v["x"], b.w_in, dn, dx, gi, bw, dskip=dres)
+    for k, want in dict(dx=dx, dgt=dgt, dwn=gn, dw_out=gw, dgate_c=gc, dw_in=gi, dW_gate=dW[0], dW_mask=dW[1],
+                        dW1=dW[2], dW3=dW[3], dW2=dW[4]).items():
+        assert torch.equal(one[k], want), k
+    # two steps without zeroing: twice the gradients
+    sink = torch.empty_like(v["x"])
+    b.backward(v["x"], one["out"], v["dout"], sink, gate_t=v["gt"], dgate_t=dgt, w_next=v["w_next"], dn_next=v["dn"],
+               dw_next=gn, seq_begin=seq, dloss=dl)
+    for k, g in b.grads.items():
+        assert torch.equal(g, 2 * one["d" + k]), k
+    # a captured step on other rows
+    keep = v["x"].clone()
+    out, n, dx2 = (torch.empty_like(keep) for _ in range(3))
+    b.zero_grad()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.forward(v["x"], out, gate_t=v["gt"], w_next=v["w_next"], n_next=n, seq_begin=seq)
+        b.backward(v["x"], out, v["dout"], dx2, gate_t=v["gt"], dgate_t=dgt, w_next=v["w_next"], dn_next=v["dn"],
+                   dw_next=gn, seq_begin=seq, dloss=dl)
+    v["x"].copy_(keep.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = dict(out=out.clone(), n_next=n.clone(), dx=dx2.clone(), **{"d" + k: g.clone() for k, g in b.grads.items()})
+    eager = step(b, v, W, dl, seq)
+    for k, want in replayed.items():
+        assert torch.equal(eager[k], want), k
+
+
+@pytest.mark.parametrize("T,masked", [(1, True), (7, True), (130, True), (33, False)])
+def test_served_with_4_bit_experts(T, masked):
+    """Every stage from the one before it: the rows and activations quantised
+    bit for bit, each product against 64 bits (the bars of the products' own
+    test), the combine in fp32; then the block around it, captured and
+    replayed."""
+    sh = inputs.Shape(256, 16, 4, 384, 1, "bf16")
+    b, v, W = parts(T, sh, "bf16", masked, 9)
+    ex = block.Mx4Experts(T, sh.d, sh.E, sh.I, sh.K, 1, *W)
+    b = block.MoeBlock(T, sh.d, sh.E, sh.I, sh.K, 1, *W, v["w_in"], v["w_out"], v["gc"], experts=ex)
+    got = step(b, v, W, back=False)
+    rt = gpu_route(ex.dsc, b.n, W[0], W[1])
+    assert np.array_equal(ex.idx.cpu().numpy(), rt["idx"])
+    counts = rt["counts"]
+    P = int(counts.sum())
+    assert int(ex.kept[0]) == P and (not masked or P < T * sh.K)
+
+    def values(pair):
+        return plain_values(pair[0][:P].cpu().numpy(), pair[1][:P].cpu().numpy())
+    wv = []
+    for w, got4 in ((W[2], ex.w1), (W[3], ex.w3), (W[4], ex.w2)):
+        c, s = plain_quantize(w.reshape(-1, w.shape[2]))
+        assert np.array_equal(got4[0].cpu().numpy(), c)
+        assert torch.equal(got4[1], tile_scales(torch.as_tensor(s, device=DEV)))
+        wv.append(plain_values(c, s).reshape(w.shape))
+    rows = np.repeat(np.arange(sh.E), counts)
+    tok = ex.pair[:P].cpu().numpy() // sh.K
+    assert torch.equal(ex.x_rows[:P], b.n[torch.as_tensor(tok, device=DEV).long()])
+    for src, dst in ((ex.x_rows, ex.x4), (ex.h, ex.h4)):
+        c, s = plain_quantize(src[:P])
+        assert np.array_equal(dst[0][:P].cpu().numpy(), c) and np.array_equal(dst[1][:P].cpu().numpy(), s)
+    a, hv = values(ex.x4), values(ex.h4)
+    dot = lambda A, Wt: np.einsum("rk,rnk->rn", A, Wt[rows])  # noqa: E731
+    g, u = dot(a, wv[0]), dot(a, wv[1])
+    eps = sh.d * 2.0 ** -23
+    dg, du = (eps * dot(np.abs(a), np.abs(w)) for w in wv[:2])
+    ref = g / (1 + np.exp(-g)) * u
+    tol = 1.1 * dg * (np.abs(u) + du) + np.abs(g) * du + 8 * U * np.abs(ref)
+    tol = tol + 2.0 ** -8 * (np.abs(ref) + tol) + 1e-37
+    assert (np.abs(ex.h[:P].double().cpu().numpy() - ref) <= tol).all()
+    y, ty = dot(hv, wv[2]), sh.I * 2.0 ** -23 * dot(np.abs(hv), np.abs(wv[2])) + 1e-37
+    yg = ex.y_rows[:P].double().cpu().numpy()
+    assert (np.abs(yg - y) <= ty).all()
+    # the combine of these rows: K products and sums in fp32, one rounding
+    ref, mag = np.zeros((T, sh.d)), np.zeros((T, sh.d))
+    for r, pair in enumerate(ex.pair[:P].cpu().numpy()):
+        term = float(ex.w.reshape(-1)[pair]) * yg[r]
+        ref[pair // sh.K] += term
+        mag[pair // sh.K] += np.abs(term)
+    assert (np.abs(b.y.double().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2 * sh.K * U * mag + 1e-37).all()
+    out, n = torch.empty_like(v["x"]), torch.empty_like(v["x"])
+    graph = torch.cuda.CUDAGraph()
+    keep = v["x"].clone()
+    with torch.cuda.graph(graph):
+        b.forward(v["x"], out, gate_t=v["gt"], w_next=v["w_next"], n_next=n)
+    v["x"].copy_(keep.flip(0) * 1.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = out.clone(), n.clone()
+    eager = step(b, v, W, back=False)
+    assert torch.equal(eager["out"], replayed[0]) and torch.equal(eager["n_next"], replayed[1])
+    assert not torch.equal(eager["out"], got["out"])
+
+
+def test_refusals():
+    sh = inputs.Shape(128, 8, 2, 128, 1, "bf16")
+    b, v, W = parts(3, sh, "bf16", True, 1)
+    with pytest.raises(ValueError):
+        b.backward(v["x"], v["x"], v["dout"], v["x"])
+    ex = block.Mx4Experts(3, sh.d, sh.E, sh.I, sh.K, 1, *W)
+    with pytest.raises(ValueError):
+        block.MoeBlock(3, sh.d, sh.E, sh.I, sh.K, 1, *W, v["w_in"], train=True, experts=ex)

@@ -188,3 +188,147 @@ def test_product_matches_fp64(counts, n, k, swiglu, out):
     y, dsc, wk = product(counts, n, k, a, ws, out)
     abi.mx4_check(dsc, wk)
     assert_product(y, counts, n, k, a, ws, out)
+
+
+# ---------------------------------------------- what is there besides values --
+
+def small(counts=(3, 0, 20), n=128, k=256, seed=1, tail=4, swiglu=False):
+    return (list(counts), n, k) + operands(list(counts), n, k, seed, swiglu=swiglu, tail=tail)
+
+
+def test_not_a_number_stays_in_its_row_and_column():
+    """A token row's block that stands for NaN makes its row NaN, a weight's its
+    column of its expert; rows behind the last expert's and other experts'
+    do not see them."""
+    counts, n, k, a, ws = small()
+    clean, _, _ = product(counts, n, k, a, ws)
+    a = (a[0], a[1].clone())
+    a[1][5, 1] = 255           # a row of expert 2
+    a[1][23:] = 255            # rows nobody owns
+    w = (ws[0][0], ws[0][1].clone())
+    w[1][7, 0] = 255           # expert 0, column 7
+    w[1][n + 9] = 255          # expert 1, without rows
+    y, dsc, wk = product(counts, n, k, a, [w])
+    abi.mx4_check(dsc, wk)
+    bad = torch.zeros(27, n, dtype=torch.bool, device=DEV)
+    bad[5], bad[:3, 7] = True, True
+    bad[23:] = False
+    assert torch.equal(torch.isnan(y), bad)
+    assert torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+def test_no_rows_and_no_capacity(swiglu):
+    counts, n, k, a, ws = small((0, 0, 0), tail=5, swiglu=swiglu)
+    y, dsc, wk = product(counts, n, k, a, ws)
+    abi.mx4_check(dsc, wk)
+    assert (y == 7.0).all()
+    empty = (a[0][:0], a[1][:0])
+    y, dsc, wk = product(counts, n, k, empty, ws)
+    abi.mx4_check(dsc, wk)
+    assert y.shape == (0, n)
+
+
+@pytest.mark.parametrize("counts", [[3, -2, 20], [30, 0, 0], [20, 5, 20], [2 ** 31 - 1, 2 ** 31 - 1, 5]])
+def test_counts_that_do_not_fit_are_cut_and_reported(counts):
+    """Negative counts and sums past N: an error, nothing written past N, rows
+    of the experts before the fault as they are; the next call is clean."""
+    good, n, k, a, ws = small()
+    N = a[0].shape[0]
+    guard = torch.full((N + 8, n), 7.0, device=DEV)
+    dsc = abi.mx4_desc(N, 3, n, k, out="f32")
+    wk = abi.alloc_mx4_workspace(dsc)
+    args = (*a,), (ws[0][0], tile_scales(ws[0][1]))
+    abi.mx4_expert_product(dsc, *args[0], torch.tensor(counts, dtype=torch.int32, device=DEV), *args[1], guard[:N], wk)
+    with pytest.raises(abi.BeamError) as e:
+        abi.mx4_check(dsc, wk)
+    assert e.value.status == 6 and (guard[N:] == 7.0).all()
+    abi.mx4_expert_product(dsc, *args[0], torch.tensor(good, dtype=torch.int32, device=DEV), *args[1], guard[:N], wk)
+    abi.mx4_check(dsc, wk)
+    clean, _, _ = product(good, n, k, a, ws)
+    assert torch.equal(guard[:23], clean[:23])
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    """A captured product follows the counts and rows of its replay, two calls
+    on two streams with a workspace each do not meet, and results repeat."""
+    counts, n, k, a, ws = small((40, 0, 200), n=384, k=512, tail=16, swiglu=True)
+    want, _, _ = product(counts, n, k, a, ws)
+    N, E = a[0].shape[0], 3
+    dsc = abi.mx4_desc(N, E, n, k, swiglu=True, out="f32")
+    scales = [tile_scales(w[1]) for w in ws]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    wks = [abi.alloc_mx4_workspace(dsc) for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, wk in zip(streams, wks):
+        with torch.cuda.stream(s):
+            y = torch.full((N, n), 7.0, device=DEV)
+        for _ in range(3):
+            abi.mx4_expert_product(dsc, *a, c, ws[0][0], scales[0], y, wk, w3_codes=ws[1][0], w3_scales=scales[1],
+                                   stream=s)
+        outs.append(y)
+    torch.cuda.synchronize()
+    for y, wk in zip(outs, wks):
+        abi.mx4_check(dsc, wk)
+        assert torch.equal(y, want)
+    codes, sc = torch.zeros_like(a[0]), torch.zeros_like(a[1])
+    cg = torch.zeros(E, dtype=torch.int32, device=DEV)
+    y = torch.full((N, n), 7.0, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        abi.mx4_expert_product(dsc, codes, sc, cg, ws[0][0], scales[0], y, wks[0], w3_codes=ws[1][0],
+                               w3_scales=scales[1])
+    codes.copy_(a[0])
+    sc.copy_(a[1])
+    for trial in (counts, [200, 40, 0], [0, 1, 0]):
+        cg.copy_(torch.tensor(trial, dtype=torch.int32))
+        y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, _, _ = product(trial, n, k, a, ws)
+        assert torch.equal(y, ref)
+
+
+def test_expired_wait_is_reported_and_the_next_call_is_clean():
+    """A stage that never fills (the library's test switch): a timeout, and the
+    workspace serves the next call."""
+    counts, n, k, a, ws = small((150, 3, 20), n=256, k=4096)
+    want, dsc, wk = product(counts, n, k, a, ws)
+    try:
+        abi.set_fault_injection(abi.FAULT_MX4_STAGE, 20_000_000)
+        _, dsc, wk = product(counts, n, k, a, ws)
+        with pytest.raises(abi.BeamError) as e:
+            abi.mx4_check(dsc, wk)
+        assert e.value.status == 5
+    finally:
+        abi.set_fault_injection(abi.FAULT_NONE, 0)
+    y, dsc, wk = product(counts, n, k, a, ws)
+    abi.mx4_check(dsc, wk)
+    assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values of rows and of outputs: the last rows are those of
+    a small call."""
+    rows, cols = 1_100_000, 2048
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[:-3] = 0.5
+    x[-3:] = rows_of(3, cols, torch.bfloat16, 4)
+    codes, scales = quantize(x)
+    c, s = quantize(x[-3:].clone())
+    assert torch.equal(codes[-3:], c) and torch.equal(scales[-3:], s)
+    abi.mx4_dequantize(codes, scales, x)
+    v = torch.empty(3, cols, dtype=torch.bfloat16, device=DEV)
+    abi.mx4_dequantize(c, s, v)
+    assert torch.equal(x[-3:], v) and (x[:-3] == 0.5).all()
+    del x, codes, scales
+    N, n, k = 70_000, 32768, 128
+    a, ws = operands([N], n, k, 2)
+    y, dsc, wk = product([N], n, k, a, ws)
+    abi.mx4_check(dsc, wk)
+    last = (a[0][-100:].clone(), a[1][-100:].clone())
+    ref, _, _ = product([100], n, k, last, ws)
+    assert torch.equal(y[-100:], ref)

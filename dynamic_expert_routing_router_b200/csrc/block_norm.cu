@@ -165,16 +165,23 @@ __device__ __forceinline__ const float *shared_by_group(Row &r) {
     return s;
 }
 
-__device__ __forceinline__ float row_sum(Row &r, float v) {
+// Two sums at once: half of the lanes carry each.
+__device__ __forceinline__ void row_sum2(Row &r, float &a, float &b) {
+    const bool up = (r.lane & 16) != 0;
+    const float other = __shfl_xor_sync(kAll, up ? a : b, 16);
+    float t = (up ? b : a) + other;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    if (r.warps == 1) return v;
-    if (r.lane == 0) r.now[r.warp] = v;
-    const float *s = shared_by_group(r);
-    v = r.lane < r.warps ? s[r.lane] : 0.0f;
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    if (r.warps > 1) {
+        if ((r.lane & 15) == 0) r.now[r.warp * 8 + (r.lane >> 4)] = t;
+        const float *s = shared_by_group(r);
+        const int w = r.lane & 15;  // at most 16 warps
+        t = w < r.warps ? s[w * 8 + (r.lane >> 4)] : 0.0f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    return __shfl_sync(kAll, v, 0);  // of lanes 0..15: at most 16 warps
+        for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    }
+    a = __shfl_sync(kAll, t, 0);
+    b = __shfl_sync(kAll, t, 16);
 }
 
 // Eight sums at once: each exchange halves the values a lane carries, nine
@@ -276,25 +283,31 @@ __global__ void __launch_bounds__(kFwThreads<NV>, NV <= 2 ? 2 : 1)
             if (wn) nw[i] = load_vec(wn + column(i));
         }
     }
+    // The square sum of the next row's y is taken before this row's out is
+    // normed, so that one reduction per row does for both.
+    auto squares = [&](int stage) {
+        float2 yy = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Vec<T> v = read_copy<THREADS, T>(base + stage + kY + i * kVec);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
+        }
+        return yy.x + yy.y;
+    };
+    const bool norm = BRANCH && w;
+    cp_async_wait_for(depth - 1);
     float gate = gt && t < rows ? to_f(gt[t]) : 0.0f;
+    float yy = norm && t < rows ? squares(0) : 0.0f, unused = 0.0f;
+    if (norm && t < rows) row_sum2(row, yy, unused);
     for (int stage = 0; t < rows; t += step, at += hop) {
-        const float z = gate;
-        if (gt && t + step < rows) gate = to_f(gt[t + step]);
-        cp_async_wait_for(depth - 1);
         float s = a.branch_scale;
         if (BRANCH) {
-            if (gt) s *= 1.0f / (1.0f + expf(-z));
-            if (w) {
-                float2 yy = both(0.0f);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const Vec<T> v = read_copy<THREADS, T>(base + stage + kY + i * kVec);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) yy = __ffma2_rn(v.two(k), v.two(k), yy);
-                }
-                s *= rsqrtf(fmaf(row_sum(row, yy.x + yy.y), inv_d, eps));
-            }
+            if (gt) s *= 1.0f / (1.0f + expf(-gate));
+            if (norm) s *= rsqrtf(fmaf(yy, inv_d, eps));
         }
+        const bool more = t + step < rows;
+        if (gt && more) gate = to_f(gt[t + step]);
         Vec<T> o[NV];
         float2 oo = both(0.0f);
         T *out = static_cast<T *>(a.out) + at;
@@ -322,8 +335,12 @@ __global__ void __launch_bounds__(kFwThreads<NV>, NV <= 2 ? 2 : 1)
         }
         fetch(stage);
         stage = stage + kStage == wrap ? 0 : stage + kStage;
+        cp_async_wait_for(depth - 1);  // the next row's copies
+        yy = norm && more ? squares(stage) : 0.0f;
+        float sum = oo.x + oo.y;
+        if (wn || norm) row_sum2(row, sum, yy);
         if (!wn) continue;
-        const float r = rsqrtf(fmaf(row_sum(row, oo.x + oo.y), inv_d, eps));
+        const float r = rsqrtf(fmaf(sum, inv_d, eps));
         T *n = static_cast<T *>(a.n) + at;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {

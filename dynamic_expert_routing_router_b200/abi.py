@@ -1,4 +1,5 @@
-"""ctypes binding of libbeam_moe.so (include/beam_moe.h).
+"""Binding of libbeam_moe.so (include/beam_moe.h): ctypes, and for the calls that
+check whole tensors the compiled module _marshal.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  Tensors are torch tensors on the current CUDA device; streams default
@@ -362,22 +363,38 @@ def ep_combine(dsc, y_rows, topk_idx, topk_w, pair_pos, out, stream=None):
 # ------------------------------------------------------ checked arguments --
 # The calls below take whole tensors, not buffers with a descriptor's word for
 # their size, so the binding refuses what the library cannot see: another
-# dtype or shape, strides, another device than the current one.
+# dtype or shape, strides, another device than the current one.  The checks and
+# the call run in the compiled module _marshal (csrc/marshal.cpp), from one
+# description of each entry point; errors are worded here.
 
 def _code(dtype):
     return dtype if isinstance(dtype, int) else (BEAM_BF16 if dtype == "bf16" else BEAM_F32)
 
 
 _torch_module = None
+_marshal_module = None
 
 
 def _torch():
-    """torch, looked up once: small calls are bound by the host's time."""
     global _torch_module
     if _torch_module is None:
         import torch
         _torch_module = torch
     return _torch_module
+
+
+def _marshal():
+    """The compiled half of the binding; raises if it was not built."""
+    global _marshal_module
+    if _marshal_module is None:
+        _torch()  # its libraries come first
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("the module _marshal is missing: build it with "
+                               "`python -m dynamic_expert_routing_router_b200.build`") from e
+        _marshal_module = m
+    return _marshal_module
 
 
 def _torch_dtype(code):
@@ -386,25 +403,87 @@ def _torch_dtype(code):
 
 def _arg(what, name, t, dtype, shape, dev, optional=False):
     """The address of tensor `t`, which has to be a contiguous `dtype` tensor
-    of `shape` on device `dev` (_current_device()); None where it may be left
-    out."""
+    of `shape` on device `dev` (_current_device(); None: anywhere); None where
+    it may be left out."""
     if t is None:
         if optional:
             return None
         raise BeamError(1, f"{what}: {name} is missing")
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise BeamError(1, f"{what}: {name} has to be a contiguous {dtype} tensor of shape "
                            f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
+    if dev is not None and t.get_device() != dev:
+        raise BeamError(1, f"{what}: {name} is on {t.device}, not the current CUDA device")
+    return t.data_ptr()
 
 
-def _workspace(what, t, dev):
-    """(address, bytes) of a uint8 workspace on device `dev`."""
-    if t is None:
-        raise BeamError(3, f"{what}: the workspace is missing")
-    return _arg(what, "workspace", t, _torch().uint8, t.shape, dev), t.numel()
+_ROWS, _F32, _I32, _U8, _WORKSPACE = range(5)
+
+
+class _Entry:
+    """An entry point f(desc, tensors..., stream) and what its tensors have to
+    be: "name dtype dim ..." each, dtype "rows" (by the descriptor's field
+    `rows`), f32, i32, u8 or "workspace" (an address and a size), dims products
+    of descriptor fields ("E*n", "k/32", "n_seq+1"); a "?" behind the name:
+    may be left out."""
+
+    _KINDS = {"rows": _ROWS, "f32": _F32, "i32": _I32, "u8": _U8, "workspace": _WORKSPACE}
+
+    def __init__(self, name, desc, rows, *tensors):
+        self.name, self.desc, self.rows, self.spec = name, desc, rows, None
+        self.fields = [f for f, _ in desc._fields_]
+        self.tensors = []
+        for t in tensors:
+            label, kind, *dims = t.split()
+            self.tensors.append((label.rstrip("?"), self._KINDS[kind], label.endswith("?"),
+                                 [self._dim(d) for d in dims]))
+
+    def _dim(self, text):
+        """(field a or -1, field b or -1, divisor, addend) of a size."""
+        if text.isdigit():
+            return (-1, -1, 1, int(text))
+        text, _, add = text.partition("+")
+        text, _, div = text.partition("/")
+        a, _, b = text.partition("*")
+        at = self.fields.index
+        return (at(a), at(b) if b else -1, int(div or 1), int(add or 0))
+
+    def compiled(self):
+        address = ctypes.cast(getattr(lib(), self.name), ctypes.c_void_p).value
+        rows = self.fields.index(self.rows) if self.rows else -1
+        self.spec = _marshal().spec(address, len(self.fields), rows,
+                                    [(kind, opt, dims) for _, kind, opt, dims in self.tensors])
+        return self.spec
+
+    def refuse(self, status, dsc, tensors):
+        """Raise for a status, or for the tensor that is not as described."""
+        if status > 0:
+            raise BeamError(status, self.name)
+        torch = _torch()
+        f = [getattr(dsc, x) for x in self.fields]
+        kinds = {_F32: torch.float32, _I32: torch.int32, _U8: torch.uint8,
+                 _WORKSPACE: torch.uint8}
+        if self.rows:
+            kinds[_ROWS] = _torch_dtype(getattr(dsc, self.rows))
+        for (_, kind, _, _), t in zip(self.tensors, tensors):
+            if kind == _WORKSPACE and t is None:
+                raise BeamError(3, f"{self.name}: the workspace is missing")
+        for dev in (None, _current_device()):
+            for (name, kind, opt, dims), t in zip(self.tensors, tensors):
+                if kind == _WORKSPACE:
+                    shape = t.shape
+                else:
+                    shape = tuple((0 if a < 0 else f[a]) * (1 if b < 0 else f[b]) // div + add
+                                  for a, b, div, add in dims)
+                _arg(self.name, name, t, kinds[kind], shape, dev, opt)
+        raise BeamError(1, self.name)
+
+
+def _call(entry, dsc, stream, *tensors):
+    status = _marshal_module.run(entry.spec or entry.compiled(), dsc, stream, *tensors) \
+        if _marshal_module else _marshal().run(entry.compiled(), dsc, stream, *tensors)
+    if status:
+        entry.refuse(status, dsc, tensors)
 
 
 def _alloc(what, n, device):
@@ -417,17 +496,26 @@ def _current_device():
     """Index of the current CUDA device.  Before CUDA is up no tensor can be on
     one: -2, which no tensor's get_device() gives."""
     torch = _torch()
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-
-
-def _stream_on(stream, dev):
-    """Raw handle of `stream`, by default the current one of device `dev`."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
 # ------------------------------------------------- the residual block around --
+
+_BLOCK_ENTER = _Entry("beam_block_enter", BlockDesc, "dtype", "x rows T d", "w rows d",
+                      "n rows T d")
+_BLOCK_EXIT = _Entry("beam_block_exit", BlockDesc, "dtype", "res rows T d", "y rows T d",
+                     "w_out? rows d", "gate_c? rows d", "gate_t? rows T", "out rows T d",
+                     "w_next? rows d", "n_next? rows T d")
+_BLOCK_ENTER_BACKWARD = _Entry("beam_block_enter_backward", BlockDesc, "dtype", "x rows T d",
+                               "w rows d", "dn f32 T d", "dskip? rows T d", "dx rows T d",
+                               "dw f32 d", "workspace workspace")
+_BLOCK_EXIT_BACKWARD = _Entry("beam_block_exit_backward", BlockDesc, "dtype", "y rows T d",
+                              "out? rows T d", "w_out? rows d", "gate_c? rows d",
+                              "gate_t? rows T", "w_next? rows d", "dout rows T d",
+                              "dn_next? f32 T d", "dres rows T d", "dy rows T d", "dw_out? f32 d",
+                              "dgate_c? f32 d", "dgate_t? f32 T", "dw_next? f32 d",
+                              "workspace workspace")
+
 
 def block_desc(T, d, dtype="bf16", eps=1e-6, res_scale=1.0, branch_scale=1.0,
                accumulate=False) -> BlockDesc:
@@ -448,11 +536,7 @@ def alloc_block_workspace(dsc: BlockDesc, device=None):
 
 def block_enter(dsc, x, w, n, stream=None):
     """n = x r(x) w, r(x) = 1 / sqrt(mean x^2 + eps) per row: what the layer reads."""
-    what, dt, dev = "beam_block_enter", _torch_dtype(dsc.dtype), _current_device()
-    rows, row = (dsc.T, dsc.d), (dsc.d,)
-    _ok(lib().beam_block_enter(dsc, _arg(what, "x", x, dt, rows, dev),
-                               _arg(what, "w", w, dt, row, dev),
-                               _arg(what, "n", n, dt, rows, dev), _stream_on(stream, dev)), what)
+    _call(_BLOCK_ENTER, dsc, stream, x, w, n)
 
 
 def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=None, n_next=None,
@@ -460,30 +544,14 @@ def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=No
     """out = res_scale res + branch_scale sigmoid(gate_t) gate_c w_out y r(y)
     (each of w_out [d], gate_c [d], gate_t [T] may be left out; without w_out y
     is not normed); with w_next also n_next = out r(out) w_next."""
-    what, dt, dev = "beam_block_exit", _torch_dtype(dsc.dtype), _current_device()
-    rows, row = (dsc.T, dsc.d), (dsc.d,)
     if (w_next is None) != (n_next is None):
-        raise BeamError(1, f"{what}: w_next and n_next go together")
-    _ok(lib().beam_block_exit(
-        dsc, _arg(what, "res", res, dt, rows, dev), _arg(what, "y", y, dt, rows, dev),
-        _arg(what, "w_out", w_out, dt, row, dev, True),
-        _arg(what, "gate_c", gate_c, dt, row, dev, True),
-        _arg(what, "gate_t", gate_t, dt, (dsc.T,), dev, True),
-        _arg(what, "out", out, dt, rows, dev), _arg(what, "w_next", w_next, dt, row, dev, True),
-        _arg(what, "n_next", n_next, dt, rows, dev, True), _stream_on(stream, dev)), what)
+        raise BeamError(1, "beam_block_exit: w_next and n_next go together")
+    _call(_BLOCK_EXIT, dsc, stream, res, y, w_out, gate_c, gate_t, out, w_next, n_next)
 
 
 def block_enter_backward(dsc, x, w, dn, dx, dw, workspace, dskip=None, stream=None):
     """dx = dskip + dn (f32, as backward's dx) through the norm; dw f32 [d]."""
-    torch = _torch()
-    what, dt, dev = "beam_block_enter_backward", _torch_dtype(dsc.dtype), _current_device()
-    rows, row, f32 = (dsc.T, dsc.d), (dsc.d,), torch.float32
-    ws, n = _workspace(what, workspace, dev)
-    _ok(lib().beam_block_enter_backward(
-        dsc, _arg(what, "x", x, dt, rows, dev), _arg(what, "w", w, dt, row, dev),
-        _arg(what, "dn", dn, f32, rows, dev), _arg(what, "dskip", dskip, dt, rows, dev, True),
-        _arg(what, "dx", dx, dt, rows, dev), _arg(what, "dw", dw, f32, row, dev), ws, n,
-        _stream_on(stream, dev)), what)
+    _call(_BLOCK_ENTER_BACKWARD, dsc, stream, x, w, dn, dskip, dx, dw, workspace)
 
 
 def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=None, w_out=None,
@@ -492,33 +560,23 @@ def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=Non
     """Gradients of block_exit for dout and, with w_next, dn_next (f32): dres
     and dy in the rows' dtype, and in f32 that of each weight and gate that is
     given (dw_out, dgate_c, dw_next [d], dgate_t [T])."""
-    torch = _torch()
-    what, dt, dev = "beam_block_exit_backward", _torch_dtype(dsc.dtype), _current_device()
-    rows, row, toks, f32 = (dsc.T, dsc.d), (dsc.d,), (dsc.T,), torch.float32
-    for name, a, b in (("w_out", w_out, dw_out), ("gate_c", gate_c, dgate_c),
-                       ("gate_t", gate_t, dgate_t), ("w_next", w_next, dw_next),
-                       ("w_next", w_next, dn_next)):
-        if (a is None) != (b is None):
-            raise BeamError(1, f"{what}: {name} and its gradient go together")
-    ws, n = _workspace(what, workspace, dev)
-    _ok(lib().beam_block_exit_backward(
-        dsc, _arg(what, "y", y, dt, rows, dev),
-        _arg(what, "out", out, dt, rows, dev, w_next is None),
-        _arg(what, "w_out", w_out, dt, row, dev, True),
-        _arg(what, "gate_c", gate_c, dt, row, dev, True),
-        _arg(what, "gate_t", gate_t, dt, toks, dev, True),
-        _arg(what, "w_next", w_next, dt, row, dev, True),
-        _arg(what, "dout", dout, dt, rows, dev),
-        _arg(what, "dn_next", dn_next, f32, rows, dev, True),
-        _arg(what, "dres", dres, dt, rows, dev), _arg(what, "dy", dy, dt, rows, dev),
-        _arg(what, "dw_out", dw_out, f32, row, dev, True),
-        _arg(what, "dgate_c", dgate_c, f32, row, dev, True),
-        _arg(what, "dgate_t", dgate_t, f32, toks, dev, True),
-        _arg(what, "dw_next", dw_next, f32, row, dev, True), ws, n, _stream_on(stream, dev)),
-        what)
+    if ((w_out is None) != (dw_out is None) or (gate_c is None) != (dgate_c is None)
+            or (gate_t is None) != (dgate_t is None) or (w_next is None) != (dw_next is None)
+            or (w_next is None) != (dn_next is None)):
+        raise BeamError(1, "beam_block_exit_backward: a weight or gate and its gradient go together")
+    _call(_BLOCK_EXIT_BACKWARD, dsc, stream, y, out, w_out, gate_c, gate_t, w_next, dout, dn_next,
+          dres, dy, dw_out, dgate_c, dgate_t, dw_next, workspace)
 
 
 # ------------------------------------------------------------ balance loss --
+
+_BALANCE = _Entry("beam_moe_balance", BalanceDesc, None, "logits f32 T logits_ld",
+                  "seq_begin? i32 n_seq+1", "loss f32 1", "cand_counts i32 n_seq E",
+                  "kept_counts? i32 n_seq E", "mean_prob? f32 n_seq E", "workspace workspace")
+_BALANCE_BACKWARD = _Entry("beam_moe_balance_backward", BalanceDesc, None,
+                           "logits f32 T logits_ld", "seq_begin? i32 n_seq+1",
+                           "counts i32 n_seq E", "dloss? f32 1", "dlogits f32 T E")
+
 
 def balance_desc(T, E, K, n_seq=1, logits_ld=None, has_mask=False, count_kept=False, tau=0.5,
                  coef=1.0) -> BalanceDesc:
@@ -544,40 +602,32 @@ def balance(dsc, logits, loss, cand_counts, workspace, kept_counts=None, mean_pr
     [T, logits_ld]; cand_counts (kept_counts) int32 [n_seq, E]: how many tokens
     of a sequence have (keep) expert e among their K candidates; mean_prob f32
     [n_seq, E] = P.  seq_begin int32 [n_seq + 1] (device)."""
-    torch = _torch()
-    what, dev, i32 = "beam_moe_balance", _current_device(), torch.int32
-    table = (dsc.n_seq, dsc.E)
     if kept_counts is not None and not dsc.has_mask:
-        raise BeamError(1, f"{what}: kept_counts without a mask")
-    ws, n = _workspace(what, workspace, dev)
-    _ok(lib().beam_moe_balance(
-        dsc, _arg(what, "logits", logits, torch.float32, (dsc.T, dsc.logits_ld), dev),
-        _arg(what, "seq_begin", seq_begin, i32, (dsc.n_seq + 1,), dev, dsc.n_seq == 1),
-        _arg(what, "loss", loss, torch.float32, (1,), dev),
-        _arg(what, "cand_counts", cand_counts, i32, table, dev),
-        _arg(what, "kept_counts", kept_counts, i32, table, dev, True),
-        _arg(what, "mean_prob", mean_prob, torch.float32, table, dev, True), ws, n,
-        _stream_on(stream, dev)), what)
+        raise BeamError(1, "beam_moe_balance: kept_counts without a mask")
+    _call(_BALANCE, dsc, stream, logits, seq_begin, loss, cand_counts, kept_counts, mean_prob,
+          workspace)
 
 
 def balance_backward(dsc, logits, counts, dlogits, seq_begin=None, dloss=None, stream=None):
     """dlogits f32 [T, E] of the balance loss, times dloss f32 [1] (device; 1 if
     left out).  counts: the forward's cand_counts, or kept_counts with
     count_kept.  backward(..., dlogits=) carries it on."""
-    torch = _torch()
-    what, dev = "beam_moe_balance_backward", _current_device()
-    f32, i32 = torch.float32, torch.int32
-    _ok(lib().beam_moe_balance_backward(
-        dsc, _arg(what, "logits", logits, f32, (dsc.T, dsc.logits_ld), dev),
-        _arg(what, "seq_begin", seq_begin, i32, (dsc.n_seq + 1,), dev, dsc.n_seq == 1),
-        _arg(what, "counts", counts, i32, (dsc.n_seq, dsc.E), dev),
-        _arg(what, "dloss", dloss, f32, (1,), dev, True),
-        _arg(what, "dlogits", dlogits, f32, (dsc.T, dsc.E), dev), _stream_on(stream, dev)), what)
+    _call(_BALANCE_BACKWARD, dsc, stream, logits, seq_begin, counts, dloss, dlogits)
 
 
 # ------------------------------------------- experts in 4-bit floating point --
 
-def _mx4_rows(what, x, codes, scales, dev):
+_MX4_PRODUCT = _Entry("beam_mx4_expert_product", Mx4Desc, "out_dtype", "a_codes u8 N k/2",
+                      "a_scales u8 N k/32", "counts i32 E", "w_codes u8 E*n k/2",
+                      "w_scales u8 E*n k/32", "w3_codes? u8 E*n k/2", "w3_scales? u8 E*n k/32",
+                      "out rows N n", "workspace workspace")
+_quantize_at = _dequantize_at = None
+
+
+def _refuse_rows(what, status, x, codes, scales, n_rows):
+    """Raise for a status, or for the tensor that is not as it has to be."""
+    if status > 0:
+        raise BeamError(status, what)
     torch = _torch()
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
         raise BeamError(1, f"{what}: a bf16 or f32 matrix is wanted, got {x.dtype} "
@@ -585,10 +635,12 @@ def _mx4_rows(what, x, codes, scales, dev):
     rows, cols = x.shape
     if cols % 32:
         raise BeamError(2, f"{what}: {cols} columns are no multiple of 32")
-    code = BEAM_BF16 if x.dtype == torch.bfloat16 else BEAM_F32
-    return (code, rows, cols, _arg(what, "values", x, x.dtype, (rows, cols), dev),
-            _arg(what, "codes", codes, torch.uint8, (rows, cols // 2), dev),
-            _arg(what, "scales", scales, torch.uint8, (rows, cols // 32), dev))
+    for dev in (None, _current_device()):
+        _arg(what, "values", x, x.dtype, (rows, cols), dev)
+        _arg(what, "codes", codes, torch.uint8, (rows, cols // 2), dev)
+        _arg(what, "scales", scales, torch.uint8, (rows, cols // 32), dev)
+        _arg(what, "n_rows", n_rows, torch.int32, (1,), dev, True)
+    raise BeamError(1, what)
 
 
 def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
@@ -596,20 +648,22 @@ def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
     scales uint8 [rows, cols / 32]; tiled: the scales in the tiles the product
     reads its weights' from.  n_rows: int32 [1] on the device, the rows that
     are there (the others are left as they are)."""
-    torch = _torch()
-    dev = _current_device()
-    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_quantize", x, codes, scales, dev)
-    pn = _arg("beam_mx4_quantize", "n_rows", n_rows, torch.int32, (1,), dev, True)
-    _ok(lib().beam_mx4_quantize(code, rows, cols, px, pn, pc, ps, int(tiled),
-                                _stream_on(stream, dev)), "beam_mx4_quantize")
+    global _quantize_at
+    if _quantize_at is None:
+        _quantize_at = ctypes.cast(lib().beam_mx4_quantize, ctypes.c_void_p).value
+    status = _marshal().rows(_quantize_at, True, x, codes, scales, n_rows, tiled, stream)
+    if status:
+        _refuse_rows("beam_mx4_quantize", status, x, codes, scales, n_rows)
 
 
 def mx4_dequantize(codes, scales, out, tiled=False, stream=None):
     """The values of an MXFP4 matrix, out [rows, cols] bf16 or f32."""
-    dev = _current_device()
-    code, rows, cols, px, pc, ps = _mx4_rows("beam_mx4_dequantize", out, codes, scales, dev)
-    _ok(lib().beam_mx4_dequantize(code, rows, cols, pc, ps, int(tiled), px,
-                                  _stream_on(stream, dev)), "beam_mx4_dequantize")
+    global _dequantize_at
+    if _dequantize_at is None:
+        _dequantize_at = ctypes.cast(lib().beam_mx4_dequantize, ctypes.c_void_p).value
+    status = _marshal().rows(_dequantize_at, False, out, codes, scales, None, tiled, stream)
+    if status:
+        _refuse_rows("beam_mx4_dequantize", status, out, codes, scales, None)
 
 
 def mx4_desc(N, E, n, k, swiglu=False, out="bf16") -> Mx4Desc:
@@ -632,23 +686,10 @@ def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, w
     """out[i] = a_i w_e^T for the rows i of expert e (grouped by expert, counts
     int32 [E] on the device), or SiLU(a_i w_e^T) * (a_i w3_e^T) when
     dsc.swiglu.  w_scales, w3_scales: tiled (mx4_quantize(..., tiled=True))."""
-    torch = _torch()
-    what, u8 = "beam_mx4_expert_product", torch.uint8
-    N, E, n, k = dsc.N, dsc.E, dsc.n, dsc.k
-    wc, ws = (E * n, k // 2), (E * n, k // 32)
-    if dsc.swiglu == 0 and (w3_codes is not None or w3_scales is not None):
-        raise BeamError(1, f"{what}: a second weight without swiglu")
-    second, dev = dsc.swiglu != 0, _current_device()
-    ws_at, ws_n = _workspace(what, workspace, dev)
-    _ok(lib().beam_mx4_expert_product(
-        dsc, _arg(what, "a_codes", a_codes, u8, (N, k // 2), dev),
-        _arg(what, "a_scales", a_scales, u8, (N, k // 32), dev),
-        _arg(what, "counts", counts, torch.int32, (E,), dev),
-        _arg(what, "w_codes", w_codes, u8, wc, dev), _arg(what, "w_scales", w_scales, u8, ws, dev),
-        _arg(what, "w3_codes", w3_codes, u8, wc, dev) if second else None,
-        _arg(what, "w3_scales", w3_scales, u8, ws, dev) if second else None,
-        _arg(what, "out", out, _torch_dtype(dsc.out_dtype), (N, n), dev), ws_at, ws_n,
-        _stream_on(stream, dev)), what)
+    if not dsc.swiglu and (w3_codes is not None or w3_scales is not None):
+        raise BeamError(1, "beam_mx4_expert_product: a second weight without swiglu")
+    _call(_MX4_PRODUCT, dsc, stream, a_codes, a_scales, counts, w_codes, w_scales, w3_codes,
+          w3_scales, out, workspace)
 
 
 def mx4_check(dsc, workspace, stream=None):

@@ -1,4 +1,5 @@
-"""Build libbeam_moe.so in-tree from csrc/*.cu for sm_100a (B200).
+"""Build libbeam_moe.so in-tree from csrc/*.cu for sm_100a (B200), and _marshal.so,
+the compiled half of the Python binding, from csrc/marshal.cpp.
 
     python -m dynamic_expert_routing_router_b200.build [--force] [--verbose]
 
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbeam_moe.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -42,7 +44,30 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """g++ against torch's own headers and libraries."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"],
+                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           *[f"-I{i}" for i in includes], "-o", MARSHAL, src, f"-L{os.path.join(root, 'lib')}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    build_marshal(force, verbose)
     if not force and not _stale():
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared",

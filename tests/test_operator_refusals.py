@@ -192,7 +192,11 @@ def test_the_binding_refuses_what_the_library_cannot_see():
     b = balance(T=4, n_seq=2, has_mask=False)
     lg, i32 = torch.zeros(4, 128), torch.int32
     u8 = torch.zeros(64, dtype=torch.uint8)
-    says("not the current", 1, abi.balance, b, lg, lg, lg, u8)
+    table = torch.zeros(2, 128, dtype=i32)
+    seq = torch.zeros(3, dtype=i32)
+    says("not the current", 1, abi.balance, b, lg, torch.zeros(1), table, u8, seq_begin=seq)
+    says("seq_begin has to be", 1, abi.balance, b, lg, torch.zeros(1), table, u8, seq_begin=seq[1:])
+    says("workspace is missing", 3, abi.balance, b, lg, torch.zeros(1), table, None)
     says("without a mask", 1, abi.balance, b, lg, lg, lg, u8, kept_counts=lg)
     says("logits has to be", 1, abi.balance_backward, b, lg[:, :64], lg, lg)
     says("logits has to be", 1, abi.balance_backward, b, lg.double(), torch.zeros(2, 128, dtype=i32), lg)
@@ -202,4 +206,4 @@ def test_the_binding_refuses_what_the_library_cannot_see():
     a, s, c = torch.zeros(4, 64).byte(), torch.zeros(4, 4).byte(), torch.zeros(2, dtype=i32)
     says("second weight without swiglu", 1, abi.mx4_expert_product, m, a, s, c, a, s, x, u8, w3_codes=a)
     says("workspace is missing", 3, abi.mx4_expert_product, m, a, s, c, a, s, x, None)
-    says("workspace is on cpu", 1, abi.mx4_expert_product, m, a[:, :32], s, c, a, s, x, u8)
+    says("a_codes has to be", 1, abi.mx4_expert_product, m, a[:, :32], s, c, a, s, x, u8)

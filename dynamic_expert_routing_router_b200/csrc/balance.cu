@@ -18,6 +18,8 @@
 //
 // Bound by instructions: about 40 per 32 logits for the K largest, the softmax
 // and the sums, against one 128-byte load.
+#include <cooperative_groups.h>
+
 #include "beam_internal.h"
 #include "beam_ptx.cuh"
 
@@ -26,6 +28,8 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBalWarps = 8;
+// Batches that one cluster takes: eight CTAs of 32 tokens, a barrier a sequence.
+constexpr int kSmallTokens = 256, kSmallSeqs = 4;
 constexpr int kMaxChunk = 1 << 18;  // tokens: a warp's counts fit 16 bits
 
 // Sequence boundaries as given, made safe: inside [0, T] and not decreasing.
@@ -119,24 +123,37 @@ __device__ __forceinline__ float kth_largest(const float (&r)[EPL], int E, int K
                         h[i + j] = fmaxf(x, y);
                         h[i + j + k] = fminf(x, y);
                     }
+    // After k rounds a lane can give K - k more: only so many are kept sorted.
     float kth = warp_max(h[0]);
     *m = kth;
-    for (int got = 0;;) {
+    int got = 0;
+    bool done = false;
+    auto take = [&](int keep) {  // the heads equal to kth, and the next kth
         const bool mine = h[0] == kth;
         got += __popc(__ballot_sync(kAll, mine));
 #pragma unroll
-        for (int i = 0; i + 1 < EPL; ++i) h[i] = mine ? h[i + 1] : h[i];
-        h[EPL - 1] = mine ? -INFINITY : h[EPL - 1];
+        for (int i = 0; i < EPL; ++i)
+            if (i < keep) h[i] = mine ? (i + 1 < EPL ? h[i + 1 < EPL ? i + 1 : 0] : -INFINITY) : h[i];
         const float next = warp_max(h[0]);
-        if (got >= K) {
-            // Exactly K reach the K-th.  (Equal values of one lane come off
-            // one by one, so one may be left.)
-            *ties = 0u;
-            if (got == K && next != kth && kth != -INFINITY) return kth;
-            break;
+        if (got < K) {
+            kth = next;
+            return false;
         }
-        kth = next;
+        // Exactly K reach the K-th.  (Equal values of one lane come off one
+        // by one, so one may be left.)
+        done = got == K && next != kth && kth != -INFINITY;
+        return true;
+    };
+    if (K <= EPL) {
+#pragma unroll
+        for (int k = 0; k < EPL; ++k)
+            if (take(EPL - k)) break;
+    } else {
+        while (!take(EPL)) {
+        }
     }
+    *ties = 0u;
+    if (done) return kth;
     // Ties: those above, then the lowest ids of the equal ones.
     int left = K;
     unsigned taken = 0u;
@@ -154,14 +171,78 @@ __device__ __forceinline__ float kth_largest(const float (&r)[EPL], int E, int K
     return NAN;  // nothing reaches it
 }
 
+// The warp's tokens t, t + kBalWarps, ... below hi: its probabilities, and its
+// counts of candidates and, above bit 16, of kept ones, are added up.
+template <int EPL>
+__device__ __forceinline__ void add_tokens(const BalanceArgs &a, bool mask, int t, int hi,
+                                           float (&acc)[EPL], unsigned (&count)[EPL]) {
+    const int lane = threadIdx.x & 31, E = a.E;
+    float r[EPL], next[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        acc[i] = 0.0f;
+        count[i] = 0u;
+    }
+    if (t < hi) load_row(a.logits + (long long)t * a.ld, E, r);
+    for (; t < hi; t += kBalWarps) {
+        const float *row = a.logits + (long long)t * a.ld;
+        if (t + kBalWarps < hi) load_row(row + (long long)kBalWarps * a.ld, E, next);
+        float m;
+        unsigned taken;
+        const float kth = kth_largest(r, E, a.K, &m, &taken);
+        // the mask's logits of the candidates alone; they arrive meanwhile
+        float z[EPL];
+        if (kth == kth) {
+            taken = 0u;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (r[i] >= kth) taken |= 1u << i;
+        }
+        if (mask) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if ((taken >> i) & 1u) z[i] = __ldcs(row + E + lane + 32 * i);
+        }
+        const float inv = softmax_row(r, m);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            acc[i] = fmaf(r[i], inv, acc[i]);
+            if ((taken >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
+            r[i] = next[i];
+        }
+    }
+}
+
+// The CTA's warps' sums of expert e, in order.
+template <int EPL>
+struct WarpSums {
+    float p[kBalWarps][32 * EPL];
+    unsigned c[kBalWarps][32 * EPL];
+    __device__ void put(const float (&acc)[EPL], const unsigned (&count)[EPL]) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            p[warp][lane + 32 * i] = acc[i];
+            c[warp][lane + 32 * i] = count[i];
+        }
+    }
+    __device__ void add(int e, float *v, int *cand, int *kept) const {
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) {
+            *v += p[w][e];
+            *cand += c[w][e] & 0xffffu;
+            *kept += c[w][e] >> 16;
+        }
+    }
+};
+
 template <int EPL>
 __global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
     balance_chunk_kernel(const BalanceArgs a) {
-    __shared__ float s_p[kBalWarps][32 * EPL];
-    __shared__ unsigned s_c[kBalWarps][32 * EPL];
+    __shared__ WarpSums<EPL> sums;
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
+    const int warp = threadIdx.x >> 5, E = a.E;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     const int t0 = blockIdx.x * a.C, t1 = min(a.T, t0 + a.C);
     const bool mask = a.has_mask && (a.kept || a.count_kept);
@@ -171,64 +252,105 @@ __global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
         const int lo = max(sp.lo, t0), hi = min(sp.hi, t1);
         if (lo >= hi) continue;
         float acc[EPL];
-        unsigned count[EPL];  // candidates, and above bit 16 kept ones
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            acc[i] = 0.0f;
-            count[i] = 0u;
-        }
-        float r[EPL], next[EPL];
-        int t = lo + warp;
-        if (t < hi) load_row(a.logits + (long long)t * a.ld, E, r);
-        for (; t < hi; t += kBalWarps) {
-            const float *row = a.logits + (long long)t * a.ld;
-            if (t + kBalWarps < hi) load_row(row + (long long)kBalWarps * a.ld, E, next);
-            float m;
-            unsigned taken;
-            const float kth = kth_largest(r, E, a.K, &m, &taken);
-            // the mask's logits of the candidates alone; they arrive meanwhile
-            float z[EPL];
-            if (kth == kth) {
-                taken = 0u;
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (r[i] >= kth) taken |= 1u << i;
-            }
-            if (mask) {
-#pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if ((taken >> i) & 1u) z[i] = __ldcs(row + E + lane + 32 * i);
-            }
-            const float inv = softmax_row(r, m);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                acc[i] = fmaf(r[i], inv, acc[i]);
-                if ((taken >> i) & 1u) count[i] += mask && z[i] >= a.thr ? 0x10001u : 1u;
-                r[i] = next[i];
-            }
-        }
+        unsigned count[EPL];
+        add_tokens(a, mask, lo + warp, hi, acc, count);
         __syncthreads();  // the previous sequence's sums are out
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            s_p[warp][lane + 32 * i] = acc[i];
-            s_c[warp][lane + 32 * i] = count[i];
-        }
+        sums.put(acc, count);
         __syncthreads();
         const long long at = ((long long)blockIdx.x + s) * E;
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             float v = 0.0f;
             int c = 0, k = 0;
-#pragma unroll
-            for (int w = 0; w < kBalWarps; ++w) {
-                v += s_p[w][e];
-                c += s_c[w][e] & 0xffffu;
-                k += s_c[w][e] >> 16;
-            }
+            sums.add(e, &v, &c, &k);
             a.part_p[at + e] = v;
             a.part_c[at + e] = c;
             if (mask) a.part_k[at + e] = k;
         }
     }
+}
+
+// Expert e of sequence s: what is written, and its term of the loss.
+__device__ __forceinline__ float finish_expert(const BalanceArgs &a, int s, int e, const Span &sp,
+                                               float p, int c, int k) {
+    const float len = float(sp.hi > sp.lo ? sp.hi - sp.lo : 1);
+    const long long o = (long long)s * a.E + e;
+    a.cand[o] = c;
+    if (a.kept) a.kept[o] = k;
+    if (a.prob) a.prob[o] = p / len;
+    return float(a.count_kept ? k : c) * float(a.E) / (float(a.K) * len) * (p / len);
+}
+
+// A small batch in one launch: one cluster, CTA r takes the tokens [r C, (r +
+// 1) C), and of each sequence in turn adds up the experts r, r + CTAs, ... of
+// all CTAs through their shared memory (two buffers in turn, so that one
+// cluster barrier per sequence does).  128 tokens of 128 experts take 5.4 us;
+// two launches took 6.6, and the host 2.5 more.
+template <int EPL>
+__global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const BalanceArgs a) {
+    namespace cg = cooperative_groups;
+    __shared__ WarpSums<EPL> sums;
+    struct Part {
+        float p[32 * EPL];
+        int c[32 * EPL], k[32 * EPL];
+    };
+    __shared__ Part part[2];
+    __shared__ float s_term;
+    cg::cluster_group cluster = cg::this_cluster();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int ctas = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+    const int t0 = rank * a.C, t1 = min(a.T, t0 + a.C);
+    const bool mask = a.has_mask && (a.kept || a.count_kept);
+    float term = 0.0f;  // of this thread's experts
+    bool bad = false;
+    for (int s = 0; s < a.S; ++s) {
+        const Span sp = span_of(a, s);
+        bad |= sp.bad;
+        float acc[EPL];
+        unsigned count[EPL];
+        add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), acc, count);
+        sums.put(acc, count);
+        __syncthreads();
+        Part &mine = part[s & 1];
+        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+            float v = 0.0f;
+            int c = 0, k = 0;
+            sums.add(e, &v, &c, &k);
+            mine.p[e] = v;
+            mine.c[e] = c;
+            mine.k[e] = k;
+        }
+        cluster.sync();
+        for (int e = rank + int(threadIdx.x) * ctas; e < a.E; e += blockDim.x * ctas) {
+            float v = 0.0f;
+            int c = 0, k = 0;
+            for (int r = 0; r < ctas; ++r) {
+                const Part *from = cluster.map_shared_rank(&mine, r);
+                v += from->p[e];
+                c += from->c[e];
+                k += from->k[e];
+            }
+            term += finish_expert(a, s, e, sp, v, c, k);
+        }
+    }
+    // the CTAs' terms, in order
+    term = warp_sum(term);
+    __syncthreads();
+    if (lane == 0) sums.p[warp][0] = term;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        term = 0.0f;
+        for (int w = 0; w < kBalWarps; ++w) term += sums.p[w][0];
+        s_term = term;
+    }
+    cluster.sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        float v = 0.0f;
+        for (int r = 0; r < ctas; ++r) v += *cluster.map_shared_rank(&s_term, r);
+        *a.loss = bad ? NAN : a.coef / float(a.S) * v;
+    }
+    cluster.sync();  // nobody leaves while its memory is read
 }
 
 // CTA (s, j): sequence s, experts [32 j, 32 j + 32); warp w adds up parts w, w
@@ -268,12 +390,7 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const BalanceArgs a
                 c += s_c[w][lane];
                 k += s_k[w][lane];
             }
-            const float len = float(sp.hi > sp.lo ? sp.hi - sp.lo : 1);
-            const long long o = (long long)s * a.E + e;
-            a.cand[o] = c;
-            if (a.kept) a.kept[o] = k;
-            if (a.prob) a.prob[o] = p / len;
-            term = float(a.count_kept ? k : c) * float(a.E) / (float(a.K) * len) * (p / len);
+            term = finish_expert(a, s, e, sp, p, c, k);
         }
         term = warp_sum(term);
         if (lane == 0) {
@@ -422,6 +539,24 @@ struct Chunks {
     }
 };
 template <int EPL>
+struct Small {
+    static cudaError_t launch(const BalanceArgs &a, int grid, cudaStream_t st) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kBalWarps * 32);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = grid;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, balance_small_kernel<EPL>, a);
+    }
+};
+template <int EPL>
 struct Grad {
     static cudaError_t launch(const BalanceArgs &a, int grid, cudaStream_t st) {
         return launch_pdl(balance_grad_kernel<EPL>, dim3(grid), dim3(256), 0, st, a);
@@ -471,6 +606,11 @@ beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
     a.kept = kept_counts;
     a.prob = mean_prob;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (desc->T <= kSmallTokens && desc->n_seq <= kSmallSeqs) {
+        const int ctas = desc->T <= 16 ? 1 : desc->T <= 32 ? 2 : desc->T <= 64 ? 4 : 8;
+        a.C = (desc->T + ctas - 1) / ctas;
+        return by_experts<Small>(desc->E, a, ctas, st) == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
+    }
     cudaError_t e = by_experts<Chunks>(desc->E, a, l.chunks > 0 ? l.chunks : 1, st);
     // warps: about the parts of a sequence of mean length, 8 to 32
     int warps = 8;

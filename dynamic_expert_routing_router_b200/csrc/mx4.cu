@@ -20,7 +20,7 @@ namespace {
 // is exact, so each value is rounded once, by the conversion.  Bound by
 // memory: kMxAhead loads of a thread are under way at a time.
 
-constexpr int kMxAhead = 4;
+constexpr int kMxAhead = 4, kMxAheadBack = 8;
 
 template <typename T>
 struct Eight;
@@ -99,10 +99,10 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, long long
     }
     const long long total = rows * (cols >> 3);  // eights; a block's four never split
     const int blocks = cols >> 5;
-    const long long step = (long long)gridDim.x * blockDim.x;
+    constexpr int step = 256;
     const unsigned quad = 0xfu << (threadIdx.x & 28);
-    for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total;
-         i0 += kMxAhead * step) {
+    for (long long i0 = (long long)blockIdx.x * (kMxAhead * step) + threadIdx.x; i0 < total;
+         i0 += (long long)gridDim.x * (kMxAhead * step)) {
         Eight<T> v[kMxAhead];
 #pragma unroll
         for (int q = 0; q < kMxAhead; ++q)
@@ -182,15 +182,15 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *code
                                                              T *out) {
     using Code = typename Piece<T>::Code;
     constexpr int kValues = 2 * int(sizeof(Code)), kPerBlock = 32 / kValues;
-    constexpr int kAhead = 2 * kMxAhead;
+    constexpr int kAhead = kMxAheadBack;
     griddep_wait();
     griddep_launch_dependents();
     const long long total = rows * (cols / kValues);
     const int blocks = cols >> 5;
-    const long long step = (long long)gridDim.x * blockDim.x;
+    constexpr int step = 256;
     const Code *in = reinterpret_cast<const Code *>(codes);
-    for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < total;
-         i0 += kAhead * step) {
+    for (long long i0 = (long long)blockIdx.x * (kAhead * step) + threadIdx.x; i0 < total;
+         i0 += (long long)gridDim.x * (kAhead * step)) {
         uint32_t c[kAhead], s[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
@@ -784,9 +784,11 @@ beam_status check_rows(int dtype, long long rows, int cols, int tiled) {
     return BEAM_OK;
 }
 
-int rows_grid(long long rows, int cols) {
-    const long long blocks = (rows * (cols / 8) + 255) / 256;
-    const long long most = 8ll * device_sm_count();  // 2048 threads per SM
+// CTAs for this many pieces of a thread's step; a few rounds of them leave the
+// SMs evenly loaded to the end (one round of 8 per SM: 6 % slower).
+int rows_grid(long long pieces, int ahead) {
+    const long long blocks = (pieces + 256 * ahead - 1) / (256 * ahead);
+    const long long most = 64ll * device_sm_count();
     return int(blocks < most ? blocks : most);
 }
 
@@ -808,7 +810,7 @@ beam_status beam_mx4_quantize(int dtype, long long rows, int cols, const void *x
         return BEAM_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(n_rows) & 3u) return BEAM_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(rows_grid(rows, cols)), block(256);
+    const dim3 grid(rows_grid(rows * (cols / 8), kMxAhead)), block(256);
     uint32_t *out = reinterpret_cast<uint32_t *>(codes);
     cudaError_t e =
         dtype == BEAM_BF16
@@ -827,7 +829,7 @@ beam_status beam_mx4_dequantize(int dtype, long long rows, int cols, const uint8
     if (!out || !codes || !scales || !aligned16(out) || !aligned16(codes) || !aligned16(scales))
         return BEAM_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(rows_grid(rows, cols)), block(256);
+    const dim3 grid(rows_grid(rows * (cols / (dtype == BEAM_BF16 ? 8 : 4)), kMxAheadBack)), block(256);
     cudaError_t e = dtype == BEAM_BF16
                         ? launch_pdl(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, st,
                                      codes, scales, rows, cols, tiled,

@@ -10,6 +10,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <memory>
+#include <utility>
 #include <vector>
 
 namespace {
@@ -38,7 +40,7 @@ void free_spec(PyObject *capsule) {
 }
 
 // spec(fn, fields, dtype_at, [(kind, optional, [(a, b, div, add), ...]), ...])
-PyObject *make_spec(PyObject *, PyObject *args) {
+PyObject *make_spec(PyObject *, PyObject *args) try {
     unsigned long long fn;
     int fields, dtype_at;
     PyObject *list;
@@ -71,7 +73,12 @@ PyObject *make_spec(PyObject *, PyObject *args) {
         PyErr_SetString(PyExc_ValueError, "too many arguments");
         return nullptr;
     }
-    return PyCapsule_New(spec.release(), kName, free_spec);
+    PyObject *capsule = PyCapsule_New(spec.get(), kName, free_spec);
+    if (capsule) spec.release();
+    return capsule;
+} catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
 }
 
 using P = void *;
@@ -102,7 +109,9 @@ at::ScalarType scalar_of(int kind) {
 bool address(PyObject *obj, at::ScalarType type, const long long *shape, size_t dims, int *device, P *out) {
     if (!THPVariable_Check(obj)) return false;
     const at::Tensor &t = THPVariable_Unpack(obj);
-    if (t.layout() != at::kStrided || t.scalar_type() != type || !t.is_cuda() || !t.is_contiguous()) return false;
+    // (a lazily negated view holds the other sign in memory)
+    if (t.layout() != at::kStrided || t.scalar_type() != type || !t.is_cuda() || !t.is_contiguous() || t.is_neg())
+        return false;
     if (shape) {
         const auto sizes = t.sizes();
         if (sizes.size() != dims) return false;

@@ -26,7 +26,7 @@ def with_fields(dsc, **kw):
 
 @pytest.mark.parametrize("bad,code", [
     (dict(T=-1), 1), (dict(d=0), 1), (dict(d=-8), 1), (dict(dtype=2), 1), (dict(eps=0.0), 1),
-    (dict(eps=-1.0), 1), (dict(eps=NAN), 1), (dict(eps=INF), 1), (dict(res_scale=NAN), 1),
+    (dict(eps=-1.0), 1), (dict(eps=NAN), 1), (dict(eps=INF), 1), (dict(eps=9e-31), 1), (dict(res_scale=NAN), 1),
     (dict(branch_scale=INF), 1), (dict(accumulate=2), 1), (dict(d=100), 2), (dict(d=16392), 2)])
 def test_block_descriptors(bad, code):
     dsc = with_fields(block(), **bad)
@@ -185,6 +185,8 @@ def test_the_binding_refuses_what_the_library_cannot_see():
     says("x has to be", 1, abi.block_enter, dsc, torch.zeros(64, 4, dtype=bf).t(), w, x)
     says("not the current CUDA device", 1, abi.block_enter, dsc, x, w, x)
     says("is missing", 1, abi.block_enter, dsc, None, w, x)
+    with pytest.raises(TypeError):
+        abi.block_enter(None, x, w, x)
     says("go together", 1, abi.block_exit, dsc, x, x, x, w_next=w)
     says("go together", 1, abi.block_exit_backward, dsc, x, x, x, x, x, w_out=w)
     says("workspace is missing", 3, abi.block_exit_backward, dsc, x, x, x, x, None)

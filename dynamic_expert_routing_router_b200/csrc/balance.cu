@@ -477,11 +477,11 @@ struct Layout {
 
 Layout layout_of(const beam_balance_desc *d) {
     Layout l;
-    // one wave of CTAs, at least two tokens per warp
+    // one wave of CTAs
     const long long ctas = (d->E > 128 ? 3ll : 4ll) * kNominalSMs;
     long long c = (d->T + ctas - 1) / ctas;
     c = (c + kBalWarps - 1) / kBalWarps * kBalWarps;
-    l.C = int(c < 2 * kBalWarps ? 2 * kBalWarps : c > kMaxChunk ? kMaxChunk : c);
+    l.C = int(c < kBalWarps ? kBalWarps : c > kMaxChunk ? kMaxChunk : c);
     l.chunks = int((d->T + (long long)l.C - 1) / l.C);
     l.slabs = (d->E + 31) / 32;
     const size_t n = (size_t(l.chunks) + size_t(d->n_seq)) * size_t(d->E) * 4;

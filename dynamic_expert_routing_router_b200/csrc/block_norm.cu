@@ -659,11 +659,16 @@ Shape shape_of(const beam_block_desc *d, bool backward) {
     const int vecs = d->d / 8, rows = (d->T + kNominalSMs - 1) / kNominalSMs;
     s.nv = 1;
     while (vecs > s.nv * threads_of(s.nv, backward)) s.nv *= 2;
-    // many rows per SM: fewer, busier warps; few: more warps, sooner done
-    if (s.nv == 1 && vecs >= 128 && rows >= 4 && d->dtype == BEAM_BF16) s.nv = 2;
+    // Many rows per SM: fewer, busier warps; few: more warps, sooner done.  8 M
+    // elements, one vector a thread against two: exit bf16 d = 2048 19.3 / 15.6
+    // us, d = 640 17.5 / 17.7, fp32 35.2 / 38.3; its backward bf16 d = 640 38.2 /
+    // 35.7, d = 112 46.7 / 63.7, fp32 d = 2048 68.3 / 62.3, d = 5000 93 / 104.
+    const bool bf16 = d->dtype == BEAM_BF16;
+    const bool two = backward ? vecs >= 64 && (bf16 || vecs <= 512) : vecs >= 112 && bf16;
+    if (s.nv == 1 && rows >= 4 && two) s.nv = 2;
     s.warps = (vecs + 32 * s.nv - 1) / (32 * s.nv);
     s.groups = threads_of(s.nv, backward) / 32 / s.warps;
-    if (s.groups > 15) s.groups = 15;  // named barriers 1..15
+    if (s.warps > 1 && s.groups > 15) s.groups = 15;  // named barriers 1..15
     // rather a row on every SM than several on a few
     s.per_sm = backward || s.nv > 2 ? 1 : 2;
     if (s.groups * s.per_sm > rows) s.groups = rows > s.per_sm ? rows / s.per_sm : 1;

@@ -684,12 +684,21 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 reg_fence_8(y8);
                 if (NUM_A == 2) reg_fence_8(v);
                 TOut *to = out + (long long)c0 * p.n;
-#pragma unroll
-                for (int c = 0; c < 8; ++c, to += p.n) {
-                    if (c0 + c >= w.rows) break;
+                auto put = [&](int c) {
                     float y = __uint_as_float(y8[c]);
                     if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
                     store_value(to, y);
+                    to += p.n;
+                };
+                // Whole eights without a compare per row; not in decode's small tiles,
+                // where the second copy of the code costs more (20.5 us for 19.4).
+                if (BN > 32 && c0 + 8 <= w.rows) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) put(c);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c0 + c < w.rows) put(c);
                 }
             }
             tc_fence_before_sync();

@@ -239,6 +239,11 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
         : "memory");
 }
 
+// The same with one column.
+__device__ __forceinline__ void tmem_ld_1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }

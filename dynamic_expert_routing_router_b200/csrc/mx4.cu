@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
-    __shared__ int s_tiles[kMaxE], s_rows[kMaxE], s_warp[2][kMxWarps];
+    __shared__ int s_tiles[kMaxE], s_rows[kMaxE];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, bad_sh;
     uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -432,53 +432,56 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // Inclusive sums over the experts of their rows and of their tiles.  Rows
-    // past p.N do not exist: counts that say otherwise are cut and reported.
-    {
-        int carry_r = 0, carry_t = 0;
-        for (int e0 = 0; e0 < p.E; e0 += kMxThreads) {
-            const int e = e0 + tid;
-            const int c = e < p.E ? p.counts[e] : 0;
-            if (c < 0 || c > p.N) bad_sh = 1;
-            int r = c < 0 ? 0 : c > p.N ? p.N : c;
-            long long sum = r;
+    // Inclusive sums over the experts of their rows and of their tiles, eight
+    // experts a lane.  Rows past p.N do not exist: counts that say otherwise
+    // are cut and reported.
+    if (warp == 0) {
+        constexpr int kPer = kMaxE / 32;
+        int r[kPer];
+        bool bad = false;
+        long long sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            // saturate: any sum past N is as good as N + 1 here
-            if (lane == 31) s_warp[0][warp] = int(sum > p.N ? p.N + 1ll : sum);
-            __syncthreads();
-            long long before = carry_r;
-            for (int w = 0; w < warp; ++w) before += s_warp[0][w];
-            const long long end = min(before + sum, (long long)p.N + 1);
-            if (end > p.N) bad_sh = 1;
-            const int hi = int(min(end, (long long)p.N));
-            const int lo = int(min(min(before + sum - r, (long long)p.N), (long long)hi));
-            int t = (hi - lo + BN - 1) / BN;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) t += v;
-            }
-            if (lane == 31) s_warp[1][warp] = t;
-            __syncthreads();
-            int tb = carry_t;
-            for (int w = 0; w < warp; ++w) tb += s_warp[1][w];
-            if (e < p.E) {
-                s_rows[e] = hi;
-                s_tiles[e] = tb + t;
-            }
-            long long all = carry_r;
-            for (int w = 0; w < kMxWarps; ++w) {
-                all += s_warp[0][w];
-                carry_t += s_warp[1][w];
-            }
-            carry_r = int(min(all, (long long)p.N + 1));
-            __syncthreads();
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane * kPer + i;
+            r[i] = e < p.E ? p.counts[e] : 0;
         }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            bad |= r[i] < 0 || r[i] > p.N;
+            r[i] = r[i] < 0 ? 0 : min(r[i], p.N);
+            sum += r[i];
+        }
+        long long end = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += v;
+        }
+        end -= sum;
+        int tiles = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int lo = int(min(end, (long long)p.N));
+            end += r[i];
+            bad |= end > p.N;
+            const int hi = int(min(end, (long long)p.N));
+            tiles += (hi - lo + BN - 1) / BN;
+            r[i] = tiles;
+            if (lane * kPer + i < p.E) s_rows[lane * kPer + i] = hi;
+        }
+        int before = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        before -= tiles;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane * kPer + i < p.E) s_tiles[lane * kPer + i] = before + r[i];
+        if (__any_sync(0xffffffffu, bad) && lane == 0) bad_sh = 1;
     }
+    __syncthreads();
     const int n_mb = p.n >> 7;
     const int n_units = s_tiles[p.E - 1] * n_mb;
     const int nkb = (p.k + kMxStepK - 1) / kMxStepK, chunks = p.k >> 7;
@@ -675,30 +678,46 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             tc_fence_after_sync();
             const uint32_t tb = tmem_base + (uint32_t(q * 32) << 16) + a * C::ACC_COLS;
             TOut *out = static_cast<TOut *>(p.out) + (long long)w.row * p.n + w.mb * 128 + q * 32 + lane;
+            if constexpr (BN == 32) {
+                // decode: few rows, and code that is fetched once per launch, so
+                // short code counts (eight columns at a time: 4.5 us for 4.2 at 8
+                // rows of 128, 20.4 for 20.2 at 154 rows of 128 experts)
+                TOut *to = out + (long long)((warp - 2) >> 2) * p.n;
 #pragma unroll 1
-            for (int c0 = ((warp - 2) >> 2) * 8; c0 < w.rows; c0 += 16) {
-                uint32_t y8[8], v[8];
-                tmem_ld_8(tb + c0, y8);
-                if (NUM_A == 2) tmem_ld_8(tb + BN + c0, v);
-                tmem_ld_wait();
-                reg_fence_8(y8);
-                if (NUM_A == 2) reg_fence_8(v);
-                TOut *to = out + (long long)c0 * p.n;
-                auto put = [&](int c) {
-                    float y = __uint_as_float(y8[c]);
-                    if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
+                for (int c = (warp - 2) >> 2; c < w.rows; c += 2, to += 2ll * p.n) {
+                    uint32_t y1, v1 = 0u;
+                    tmem_ld_1(tb + c, y1);
+                    if (NUM_A == 2) tmem_ld_1(tb + BN + c, v1);
+                    tmem_ld_wait();
+                    asm volatile("" : "+r"(y1), "+r"(v1));
+                    float y = __uint_as_float(y1);
+                    if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v1);
                     store_value(to, y);
-                    to += p.n;
-                };
-                // Whole eights without a compare per row; not in decode's small tiles,
-                // where the second copy of the code costs more (20.5 us for 19.4).
-                if (BN > 32 && c0 + 8 <= w.rows) {
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = ((warp - 2) >> 2) * 8; c0 < w.rows; c0 += 16) {
+                    uint32_t y8[8], v[8];
+                    tmem_ld_8(tb + c0, y8);
+                    if (NUM_A == 2) tmem_ld_8(tb + BN + c0, v);
+                    tmem_ld_wait();
+                    reg_fence_8(y8);
+                    if (NUM_A == 2) reg_fence_8(v);
+                    TOut *to = out + (long long)c0 * p.n;
+                    auto put = [&](int c) {
+                        float y = __uint_as_float(y8[c]);
+                        if (NUM_A == 2) y = y / (1.0f + expf(-y)) * __uint_as_float(v[c]);
+                        store_value(to, y);
+                        to += p.n;
+                    };
+                    if (c0 + 8 <= w.rows) {  // without a compare per row
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) put(c);
-                } else {
+                        for (int c = 0; c < 8; ++c) put(c);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c0 + c < w.rows) put(c);
+                        for (int c = 0; c < 8; ++c)
+                            if (c0 + c < w.rows) put(c);
+                    }
                 }
             }
             tc_fence_before_sync();

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
         int c[32 * EPL], k[32 * EPL];
     };
     __shared__ Part part[2];
-    __shared__ float s_term;
+    __shared__ float s_terms[8];  // of rank 0: the CTAs' terms
     cg::cluster_group cluster = cg::this_cluster();
     griddep_wait();
     griddep_launch_dependents();
@@ -342,15 +342,14 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
     if (threadIdx.x == 0) {
         term = 0.0f;
         for (int w = 0; w < kBalWarps; ++w) term += sums.p[w][0];
-        s_term = term;
+        *cluster.map_shared_rank(&s_terms[rank], 0) = term;
     }
-    cluster.sync();
+    cluster.sync();  // and nobody's part is read any more
     if (rank == 0 && threadIdx.x == 0) {
         float v = 0.0f;
-        for (int r = 0; r < ctas; ++r) v += *cluster.map_shared_rank(&s_term, r);
+        for (int r = 0; r < ctas; ++r) v += s_terms[r];
         *a.loss = bad ? NAN : a.coef / float(a.S) * v;
     }
-    cluster.sync();  // nobody leaves while its memory is read
 }
 
 // CTA (s, j): sequence s, experts [32 j, 32 j + 32); warp w adds up parts w, w

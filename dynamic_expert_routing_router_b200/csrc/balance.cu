@@ -16,8 +16,9 @@
 // token's logits being loaded meanwhile; a second launch adds the parts up.
 // Every sum runs in a fixed order: the loss is bitwise repeatable.
 //
-// Bound by instructions: about 40 per 32 logits for the K largest, the softmax
-// and the sums, against one 128-byte load.
+// Bound by instructions: about 515 a token of 256 experts, half of them for the
+// 8 largest, against two 1 KB loads.  32768 such tokens take 30 us (2.2 TB/s),
+// the second launch 5.5 of them; the gradient of 17937 x 239 9 us (3.8 TB/s).
 #include <cooperative_groups.h>
 
 #include "beam_internal.h"

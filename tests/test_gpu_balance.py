@@ -118,6 +118,27 @@ def test_gradient_is_the_difference_of_the_loss():
     assert abs(float((dl.double() * v).sum()) - want) <= 1e-5 * float(loss)
 
 
+def test_gradient_where_it_almost_cancels():
+    """Every expert a candidate (f = 1 everywhere: the gradient is 0), and one
+    expert with nearly all of the probability: relative to p_e |f_e - f_e'| p_e'
+    summed over e', not to f itself.  (The reference is that sum with signs: f -
+    <f, p> in 64 bits is off by f 2^-53 = 9e-16, against 2e-12 here.)"""
+    T, E = 9, 16
+    lg = logits_of(T, E, 5, False)
+    cand = torch.full((1, E), T, dtype=torch.int32, device=DEV)
+    dl = torch.full((T, E), float("nan"), device=DEV)
+    abi.balance_backward(abi.balance_desc(T, E, E), lg, cand, dl)
+    assert (dl == 0).all()
+    lg[:, 3] += 30.0
+    dsc = abi.balance_desc(T, E, 2)
+    abi.balance(dsc, lg, torch.empty(1, device=DEV), cand, abi.alloc_balance_workspace(dsc))
+    abi.balance_backward(dsc, lg, cand, dl)
+    f, p = cand[0].double() * E / (2 * T), torch.softmax(lg.double(), 1)
+    apart = p[:, None, :] * (f[:, None] - f[None, :])
+    g, spread = apart.sum(2) * p / T, apart.abs().sum(2) * p / T
+    assert ((dl.double() - g).abs() <= 150 * U * spread + 1e-38).all()
+
+
 @pytest.mark.parametrize("copies", [1, 100])  # one launch, and chunks
 def test_ties_infinities_and_rows_without_a_softmax(copies):
     """Equal logits count for the lower ids, -inf logits weigh nothing, a row

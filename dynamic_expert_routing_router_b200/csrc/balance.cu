@@ -449,12 +449,12 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) 
             const bool in = s < a.S && sp.lo <= t;
             ends = in || s >= a.S ? sp.hi : sp.lo;
             const float len = float(sp.hi - sp.lo);
-            const float even = float(a.K) * len;
+            const float scale = float(E) / (float(a.K) * len);
             g = in ? up / len : 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 f[i] = in && lane + 32 * i < E
-                           ? float(a.counts[(long long)s * E + lane + 32 * i]) * float(E) / even
+                           ? float(a.counts[(long long)s * E + lane + 32 * i]) * scale
                            : 0.0f;
         }
         float r[EPL], m = -INFINITY, dot = 0.0f;
@@ -464,31 +464,26 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const BalanceArgs a) 
             m = fmaxf(m, r[i]);
         }
         if (t + 1 < t1) load_row(a.logits + (long long)(t + 1) * a.ld, E, next);
-        m = warp_max(m);
-        // The probabilities add up to 1, so f may be taken less its value f0 at
-        // the likeliest expert: f - f0 - <f - f0, p> has digits left where that
-        // expert's p is almost 1, or f the same everywhere.
-        float f0 = 0.0f;
-        bool top = false;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (r[i] == m) {
-                f0 = f[i];
-                top = true;
-            }
-        f0 = __shfl_sync(kAll, f0, __ffs(__ballot_sync(kAll, top)) - 1);
-        const float inv = softmax_row(r, m);
+        const float inv = softmax_row(r, warp_max(m));
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             r[i] *= inv;
-            dot = fmaf(f[i] - f0, r[i], dot);
+            dot = fmaf(f[i], r[i], dot);
         }
         dot = warp_sum(dot);
+        // The probabilities add up to 1, so f may be taken less any f0: f - f0 -
+        // <f - f0, p>.  With <f, p> as it came out for f0, its own error cancels,
+        // and digits are left where one expert has nearly all of the probability
+        // or f is the same everywhere.
+        float rest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) rest = fmaf(f[i] - dot, r[i], rest);
+        rest = warp_sum(rest);
         float *out = a.dlogits + (long long)t * E;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (lane + 32 * i < E)
-                out[lane + 32 * i] = g == 0.0f ? 0.0f : g * r[i] * (f[i] - f0 - dot);
+                out[lane + 32 * i] = g == 0.0f ? 0.0f : g * r[i] * (f[i] - dot - rest);
     }
 }
 

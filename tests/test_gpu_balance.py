@@ -119,7 +119,8 @@ def test_gradient_is_the_difference_of_the_loss():
 
 
 def test_gradient_where_it_almost_cancels():
-    """Every expert a candidate (f = 1 everywhere: the gradient is 0), and one
+    """Every expert a candidate (f = 1 everywhere: the gradient is 0 but
+    for the second order), and one
     expert with nearly all of the probability: relative to p_e |f_e - f_e'| p_e'
     summed over e', not to f itself.  (The reference is that sum with signs: f -
     <f, p> in 64 bits is off by f 2^-53 = 9e-16, against 2e-12 here.)"""
@@ -128,7 +129,8 @@ def test_gradient_where_it_almost_cancels():
     cand = torch.full((1, E), T, dtype=torch.int32, device=DEV)
     dl = torch.full((T, E), float("nan"), device=DEV)
     abi.balance_backward(abi.balance_desc(T, E, E), lg, cand, dl)
-    assert (dl == 0).all()
+    # <f, p> is off by 60 u, and what is left of it by its own 73 u
+    assert (dl.abs().double() <= 60 * 133 * U * U * torch.softmax(lg.double(), 1) / T).all()
     lg[:, 3] += 30.0
     dsc = abi.balance_desc(T, E, 2)
     abi.balance(dsc, lg, torch.empty(1, device=DEV), cand, abi.alloc_balance_workspace(dsc))

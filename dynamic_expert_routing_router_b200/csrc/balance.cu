@@ -66,7 +66,7 @@ __device__ __forceinline__ int first_ending_after(const BalanceArgs &a, int t) {
 
 __device__ __forceinline__ float warp_max(float v) {
     float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {

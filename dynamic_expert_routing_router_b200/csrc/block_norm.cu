@@ -219,8 +219,8 @@ __device__ __forceinline__ void row_sum8(Row &r, float (&v)[8]) {
 
 // ------------------------------------------------------------- forward --
 // Weights stay in registers where a thread has one or two vectors; the pair w,
-// gate_c is multiplied once.  A thread's fixed costs per row (addresses, two
-// reductions) are as large as the arithmetic of eight elements: hence up to
+// gate_c is multiplied once.  A thread's fixed costs per row (addresses, the
+// reduction) are as large as the arithmetic of eight elements: hence up to
 // four vectors a thread.  Two CTAs of 448 threads leave a thread 72 registers,
 // which hold two bf16 vectors' state; with 512 (64 registers) some of it
 // spilled.

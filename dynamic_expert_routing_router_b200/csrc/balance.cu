@@ -17,8 +17,8 @@
 // Every sum runs in a fixed order: the loss is bitwise repeatable.
 //
 // Bound by instructions: about 515 a token of 256 experts, half of them for the
-// 8 largest, against two 1 KB loads.  32768 such tokens take 30 us (2.2 TB/s),
-// the second launch 5.5 of them; the gradient of 17937 x 239 9 us (3.8 TB/s).
+// 8 largest, against two 1 KB loads.  32768 such tokens take 28.5 us (2.4 TB/s),
+// the second launch 5 of them; the gradient of 17937 x 239 9 us (3.8 TB/s).
 #include <cooperative_groups.h>
 
 #include "beam_internal.h"
@@ -494,10 +494,10 @@ struct Layout {
 
 Layout layout_of(const beam_balance_desc *d) {
     Layout l;
-    // one wave of CTAs
+    // one wave of CTAs (chunks of whole rounds of warps left a third of the SMs
+    // a CTA short: 30.2 us for 28.5)
     const long long ctas = (d->E > 128 ? 3ll : 4ll) * kNominalSMs;
     long long c = (d->T + ctas - 1) / ctas;
-    c = (c + kBalWarps - 1) / kBalWarps * kBalWarps;
     l.C = int(c < kBalWarps ? kBalWarps : c > kMaxChunk ? kMaxChunk : c);
     l.chunks = int((d->T + (long long)l.C - 1) / l.C);
     l.slabs = (d->E + 31) / 32;

@@ -9,6 +9,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -430,7 +431,8 @@ class _Entry:
     _KINDS = {"rows": _ROWS, "f32": _F32, "i32": _I32, "u8": _U8, "workspace": _WORKSPACE}
 
     def __init__(self, name, desc, rows, *tensors):
-        self.name, self.desc, self.rows, self.spec = name, desc, rows, None
+        self.name, self.rows = name, rows
+        self.run = self._first  # (desc, stream, tensors...) -> status
         self.fields = [f for f, _ in desc._fields_]
         self.tensors = []
         for t in tensors:
@@ -448,12 +450,14 @@ class _Entry:
         at = self.fields.index
         return (at(a), at(b) if b else -1, int(div or 1), int(add or 0))
 
-    def compiled(self):
+    def _first(self, *args):
         address = ctypes.cast(getattr(lib(), self.name), ctypes.c_void_p).value
         rows = self.fields.index(self.rows) if self.rows else -1
-        self.spec = _marshal().spec(address, len(self.fields), rows,
-                                    [(kind, opt, dims) for _, kind, opt, dims in self.tensors])
-        return self.spec
+        m = _marshal()
+        self.run = functools.partial(m.run, m.spec(
+            address, len(self.fields), rows,
+            [(kind, opt, dims) for _, kind, opt, dims in self.tensors]))
+        return self.run(*args)
 
     def refuse(self, status, dsc, tensors):
         """Raise for a status, or for the tensor that is not as described."""
@@ -477,13 +481,6 @@ class _Entry:
                                   for a, b, div, add in dims)
                 _arg(self.name, name, t, kinds[kind], shape, dev, opt)
         raise BeamError(1, self.name)
-
-
-def _call(entry, dsc, stream, *tensors):
-    status = _marshal_module.run(entry.spec or entry.compiled(), dsc, stream, *tensors) \
-        if _marshal_module else _marshal().run(entry.compiled(), dsc, stream, *tensors)
-    if status:
-        entry.refuse(status, dsc, tensors)
 
 
 def _alloc(what, n, device):
@@ -536,7 +533,9 @@ def alloc_block_workspace(dsc: BlockDesc, device=None):
 
 def block_enter(dsc, x, w, n, stream=None):
     """n = x r(x) w, r(x) = 1 / sqrt(mean x^2 + eps) per row: what the layer reads."""
-    _call(_BLOCK_ENTER, dsc, stream, x, w, n)
+    status = _BLOCK_ENTER.run(dsc, stream, x, w, n)
+    if status:
+        _BLOCK_ENTER.refuse(status, dsc, (x, w, n))
 
 
 def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=None, n_next=None,
@@ -546,12 +545,16 @@ def block_exit(dsc, res, y, out, w_out=None, gate_c=None, gate_t=None, w_next=No
     is not normed); with w_next also n_next = out r(out) w_next."""
     if (w_next is None) != (n_next is None):
         raise BeamError(1, "beam_block_exit: w_next and n_next go together")
-    _call(_BLOCK_EXIT, dsc, stream, res, y, w_out, gate_c, gate_t, out, w_next, n_next)
+    status = _BLOCK_EXIT.run(dsc, stream, res, y, w_out, gate_c, gate_t, out, w_next, n_next)
+    if status:
+        _BLOCK_EXIT.refuse(status, dsc, (res, y, w_out, gate_c, gate_t, out, w_next, n_next))
 
 
 def block_enter_backward(dsc, x, w, dn, dx, dw, workspace, dskip=None, stream=None):
     """dx = dskip + dn (f32, as backward's dx) through the norm; dw f32 [d]."""
-    _call(_BLOCK_ENTER_BACKWARD, dsc, stream, x, w, dn, dskip, dx, dw, workspace)
+    status = _BLOCK_ENTER_BACKWARD.run(dsc, stream, x, w, dn, dskip, dx, dw, workspace)
+    if status:
+        _BLOCK_ENTER_BACKWARD.refuse(status, dsc, (x, w, dn, dskip, dx, dw, workspace))
 
 
 def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=None, w_out=None,
@@ -564,8 +567,13 @@ def block_exit_backward(dsc, y, dout, dres, dy, workspace, out=None, dn_next=Non
             or (gate_t is None) != (dgate_t is None) or (w_next is None) != (dw_next is None)
             or (w_next is None) != (dn_next is None)):
         raise BeamError(1, "beam_block_exit_backward: a weight or gate and its gradient go together")
-    _call(_BLOCK_EXIT_BACKWARD, dsc, stream, y, out, w_out, gate_c, gate_t, w_next, dout, dn_next,
-          dres, dy, dw_out, dgate_c, dgate_t, dw_next, workspace)
+    status = _BLOCK_EXIT_BACKWARD.run(dsc, stream, y, out, w_out, gate_c, gate_t, w_next, dout,
+                                      dn_next, dres, dy, dw_out, dgate_c, dgate_t, dw_next,
+                                      workspace)
+    if status:
+        _BLOCK_EXIT_BACKWARD.refuse(status, dsc, (y, out, w_out, gate_c, gate_t, w_next, dout,
+                                    dn_next, dres, dy, dw_out, dgate_c, dgate_t, dw_next,
+                                    workspace))
 
 
 # ------------------------------------------------------------ balance loss --
@@ -604,15 +612,20 @@ def balance(dsc, logits, loss, cand_counts, workspace, kept_counts=None, mean_pr
     [n_seq, E] = P.  seq_begin int32 [n_seq + 1] (device)."""
     if kept_counts is not None and not dsc.has_mask:
         raise BeamError(1, "beam_moe_balance: kept_counts without a mask")
-    _call(_BALANCE, dsc, stream, logits, seq_begin, loss, cand_counts, kept_counts, mean_prob,
-          workspace)
+    status = _BALANCE.run(dsc, stream, logits, seq_begin, loss, cand_counts, kept_counts,
+                          mean_prob, workspace)
+    if status:
+        _BALANCE.refuse(status, dsc, (logits, seq_begin, loss, cand_counts, kept_counts,
+                        mean_prob, workspace))
 
 
 def balance_backward(dsc, logits, counts, dlogits, seq_begin=None, dloss=None, stream=None):
     """dlogits f32 [T, E] of the balance loss, times dloss f32 [1] (device; 1 if
     left out).  counts: the forward's cand_counts, or kept_counts with
     count_kept.  backward(..., dlogits=) carries it on."""
-    _call(_BALANCE_BACKWARD, dsc, stream, logits, seq_begin, counts, dloss, dlogits)
+    status = _BALANCE_BACKWARD.run(dsc, stream, logits, seq_begin, counts, dloss, dlogits)
+    if status:
+        _BALANCE_BACKWARD.refuse(status, dsc, (logits, seq_begin, counts, dloss, dlogits))
 
 
 # ------------------------------------------- experts in 4-bit floating point --
@@ -621,7 +634,19 @@ _MX4_PRODUCT = _Entry("beam_mx4_expert_product", Mx4Desc, "out_dtype", "a_codes 
                       "a_scales u8 N k/32", "counts i32 E", "w_codes u8 E*n k/2",
                       "w_scales u8 E*n k/32", "w3_codes? u8 E*n k/2", "w3_scales? u8 E*n k/32",
                       "out rows N n", "workspace workspace")
-_quantize_at = _dequantize_at = None
+
+
+def _rows_call(name, quantize):
+    """A call that finds its entry point when it first runs."""
+    def first(*args):
+        address = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+        _rows_run[quantize] = functools.partial(_marshal().rows, address, quantize)
+        return _rows_run[quantize](*args)
+    return first
+
+
+_rows_run = {True: _rows_call("beam_mx4_quantize", True),
+             False: _rows_call("beam_mx4_dequantize", False)}
 
 
 def _refuse_rows(what, status, x, codes, scales, n_rows):
@@ -648,20 +673,14 @@ def mx4_quantize(x, codes, scales, n_rows=None, tiled=False, stream=None):
     scales uint8 [rows, cols / 32]; tiled: the scales in the tiles the product
     reads its weights' from.  n_rows: int32 [1] on the device, the rows that
     are there (the others are left as they are)."""
-    global _quantize_at
-    if _quantize_at is None:
-        _quantize_at = ctypes.cast(lib().beam_mx4_quantize, ctypes.c_void_p).value
-    status = _marshal().rows(_quantize_at, True, x, codes, scales, n_rows, tiled, stream)
+    status = _rows_run[True](x, codes, scales, n_rows, tiled, stream)
     if status:
         _refuse_rows("beam_mx4_quantize", status, x, codes, scales, n_rows)
 
 
 def mx4_dequantize(codes, scales, out, tiled=False, stream=None):
     """The values of an MXFP4 matrix, out [rows, cols] bf16 or f32."""
-    global _dequantize_at
-    if _dequantize_at is None:
-        _dequantize_at = ctypes.cast(lib().beam_mx4_dequantize, ctypes.c_void_p).value
-    status = _marshal().rows(_dequantize_at, False, out, codes, scales, None, tiled, stream)
+    status = _rows_run[False](out, codes, scales, None, tiled, stream)
     if status:
         _refuse_rows("beam_mx4_dequantize", status, out, codes, scales, None)
 
@@ -688,8 +707,11 @@ def mx4_expert_product(dsc, a_codes, a_scales, counts, w_codes, w_scales, out, w
     dsc.swiglu.  w_scales, w3_scales: tiled (mx4_quantize(..., tiled=True))."""
     if not dsc.swiglu and (w3_codes is not None or w3_scales is not None):
         raise BeamError(1, "beam_mx4_expert_product: a second weight without swiglu")
-    _call(_MX4_PRODUCT, dsc, stream, a_codes, a_scales, counts, w_codes, w_scales, w3_codes,
-          w3_scales, out, workspace)
+    status = _MX4_PRODUCT.run(dsc, stream, a_codes, a_scales, counts, w_codes, w_scales, w3_codes,
+                              w3_scales, out, workspace)
+    if status:
+        _MX4_PRODUCT.refuse(status, dsc, (a_codes, a_scales, counts, w_codes, w_scales, w3_codes,
+                            w3_scales, out, workspace))
 
 
 def mx4_check(dsc, workspace, stream=None):

@@ -660,7 +660,7 @@ int threads_of(int nv, bool backward) {
 
 Shape shape_of(const beam_block_desc *d, bool backward) {
     Shape s;
-    const int vecs = d->d / 8, rows = (d->T + kNominalSMs - 1) / kNominalSMs;
+    const int vecs = d->d / 8, rows = d->T / kNominalSMs + (d->T % kNominalSMs != 0);
     s.nv = 1;
     while (vecs > s.nv * threads_of(s.nv, backward)) s.nv *= 2;
     // Many rows per SM: fewer, busier warps; few: more warps, sooner done.  8 M

@@ -142,6 +142,11 @@ bool stream_of(PyObject *stream, int device, P *out) {
     return !PyErr_Occurred();
 }
 
+struct Buffer {  // given back on every way out, a torch error's too
+    Py_buffer view;
+    ~Buffer() { PyBuffer_Release(&view); }
+};
+
 // run(spec, descriptor, stream, tensors...): the entry point's status, or
 // -(i + 1) where tensor i is not what the descriptor asks for.
 PyObject *run(PyObject *, PyObject *const *argv, Py_ssize_t argc) {
@@ -155,7 +160,8 @@ PyObject *run(PyObject *, PyObject *const *argv, Py_ssize_t argc) {
         PyErr_SetString(PyExc_TypeError, "another number of tensors");
         return nullptr;
     }
-    Py_buffer view;
+    Buffer held = {};
+    Py_buffer &view = held.view;
     if (PyObject_GetBuffer(argv[1], &view, PyBUF_SIMPLE)) return nullptr;
     const int *f = static_cast<const int *>(view.buf);
     int status = 0, device = -1, n = 0;
@@ -187,15 +193,11 @@ PyObject *run(PyObject *, PyObject *const *argv, Py_ssize_t argc) {
             v[n++] = reinterpret_cast<P>(THPVariable_Unpack(obj).numel());
     }
     if (status == 0) {
-        if (!stream_of(argv[2], device, &v[n++])) {
-            PyBuffer_Release(&view);
-            return nullptr;
-        }
+        if (!stream_of(argv[2], device, &v[n++])) return nullptr;
         Py_BEGIN_ALLOW_THREADS;  // a full launch queue may make it wait
         status = call(spec->fn, v, n);
         Py_END_ALLOW_THREADS;
     }
-    PyBuffer_Release(&view);
     return PyLong_FromLong(status);
 }
 

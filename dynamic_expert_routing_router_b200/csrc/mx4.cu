@@ -409,6 +409,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __shared__ int s_tiles[kMaxE], s_rows[kMaxE];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, bad_sh;
+    // What an abort has to wait for: the stages issued, and the step that each
+    // scale warp gave up at (none: all of its stages are laid out).
+    __shared__ uint32_t issued_sh, gave_up_sh[kMxScaleWarps];
     uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const volatile int *abort_flag = &abort_sh;
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
         bad_sh = 0;
+        for (int i = 0; i < kMxScaleWarps; ++i) gave_up_sh[i] = ~0u;
         fence_barrier_init();
         tma_prefetch_desc(&maps.w);
         tma_prefetch_desc(&maps.a);
@@ -527,15 +531,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 __syncwarp();
             }
         }
-        if (!ok) {
-            *reinterpret_cast<volatile int *>(&abort_sh) = 1;
-            // Let this CTA's own copies land before it can exit.  A stage
-            // whose scales never came does not complete: its wait is bounded.
-            const uint32_t open = it < uint32_t(STAGES) ? it : uint32_t(STAGES);
-            for (uint32_t j = it - open; j < it; ++j)
-                mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
-                                  p.timeout_ns);
-        }
+        if (!ok) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+        if (lane == 0) issued_sh = it;
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
         const uint32_t one = elect_one();
@@ -666,7 +663,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             ring.s = s;
             it = then;
         }
-        if (!ok && lane == 0) *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+        if (!ok && lane == 0) {
+            *reinterpret_cast<volatile int *>(&abort_sh) = 1;
+            gave_up_sh[first] = it;
+        }
     } else {
         // -------------------------------------------------------- epilogue --
         const int q = warp & 3;  // TMEM lane quadrant of this warp
@@ -738,6 +738,22 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         p.status[64 + blockIdx.x] =
             abort_sh ? int(DEV_ERR_TIMEOUT) : bad_sh ? int(DEV_ERR_INTERNAL) : int(DEV_OK);
         if (blockIdx.x == 0) p.status[0] = int(gridDim.x);
+        // Whichever role gave up, this CTA's own copies land before it exits.
+        // A stage completes with its bytes and its scales' arrival, which is
+        // made here for the scale warps that left before it (nobody reads the
+        // scales any more); the waits share one limit.
+        if (abort_sh) {
+            const uint32_t n = issued_sh;
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t j = n > uint32_t(STAGES) ? n - STAGES : 0u; j < n; ++j) {
+                if (p.fault_skip && blockIdx.x == 0 && j == 0) continue;  // never issued
+                const uint32_t s = j % STAGES;
+                if (j >= gave_up_sh[s % kMxScaleWarps]) mbar_arrive(&full_bar[s]);
+                const uint64_t spent = globaltimer_ns() - t0;
+                mbar_wait_bounded(&full_bar[s], (j / STAGES) & 1u, nullptr,
+                                  spent < p.timeout_ns ? p.timeout_ns - spent : 0u);
+            }
+        }
     }
     if (warp == 1) {
         __syncwarp();

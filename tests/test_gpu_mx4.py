@@ -12,6 +12,8 @@ at most 1.1, so an error of dg in the gate and du in the up value moves
 g s(g) u by at most 1.1 dg |u| + |g| du, plus 8 2^-24 of the result for the
 exponential, division and products.
 """
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -332,3 +334,32 @@ def test_offsets_past_32_bits():
     last = (a[0][-100:].clone(), a[1][-100:].clone())
     ref, _, _ = product([100], n, k, last, ws)
     assert torch.equal(y[-100:], ref)
+
+
+@pytest.mark.parametrize("k", [1024, 8192])
+def test_a_call_that_gives_up_waits_for_its_copies_and_for_nothing_else(k):
+    """A stage that never fills, with every other stage issued before the wait
+    runs out (k = 1024: four stages in all) and with more stages than the ring
+    holds: one wait limit passes, not another one for the stage that never
+    comes, and the next call is clean."""
+    counts, n, k, a, ws = small((20,), k=k)
+    want, dsc, wk = product(counts, n, k, a, ws)
+    limit = 0.2
+    c = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    y, tiled = torch.empty_like(want), tile_scales(ws[0][1])
+    torch.cuda.synchronize()
+    try:
+        abi.set_fault_injection(abi.FAULT_MX4_STAGE, int(limit * 1e9))
+        begin = time.perf_counter()
+        abi.mx4_expert_product(dsc, *a, c, ws[0][0], tiled, y, wk)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - begin
+    finally:
+        abi.set_fault_injection(abi.FAULT_NONE, 0)
+    with pytest.raises(abi.BeamError) as e:
+        abi.mx4_check(dsc, wk)
+    assert e.value.status == 5 and limit <= took < 1.8 * limit, took
+    y.fill_(7.0)
+    abi.mx4_expert_product(dsc, *a, c, ws[0][0], tiled, y, wk)
+    abi.mx4_check(dsc, wk)
+    assert torch.equal(y, want)

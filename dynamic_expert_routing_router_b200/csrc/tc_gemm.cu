@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
+    __shared__ uint32_t issued_sh;  // stages the producer issued
     constexpr bool DYN = MODE == MODE_EXPERTS;  // dynamic unit hand-out
     constexpr int kRing = 4;
     __shared__ int unit_ring[kRing];
@@ -365,13 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
             }
-            if (!ok) {
-                signal_abort(p, &abort_sh);
-                // Let this CTA's own copies land before it can exit.
-                for (uint32_t j = (it > uint32_t(STAGES) ? it - STAGES : 0u); j < it; ++j)
-                    mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
-                                      p.timeout_ns);
-            }
+            if (!ok) signal_abort(p, &abort_sh);
+            issued_sh = it;
         }
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer --
@@ -583,6 +579,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before_sync();
     __syncthreads();
+    // Whichever role gave up, this CTA's own copies land before it exits; the
+    // waits share one limit.
+    if (threadIdx.x == 0 && abort_sh) {
+        const uint32_t n = issued_sh;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t j = n > uint32_t(STAGES) ? n - STAGES : 0u; j < n; ++j) {
+            if (p.fault_skip && blockIdx.x == 0 && j == 0) continue;  // never issued
+            const uint64_t spent = globaltimer_ns() - t0;
+            mbar_wait_bounded(&full_bar[j % STAGES], (j / STAGES) & 1u, nullptr,
+                              spent < p.timeout_ns ? p.timeout_ns - spent : 0u);
+        }
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after_sync();

@@ -11,6 +11,8 @@
   workspace sit between canary words; route, forward, forward with shared
   experts and backward on ragged shapes must leave every canary unchanged.
 """
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -239,3 +241,30 @@ def test_guard_bands_route_forward_backward(name, T, d, E, I, K, renorm, f, dt):
     # the inputs themselves are unchanged
     for a, b in ((xg, x), (Wgg, Wg), (Wmg, Wm), (W1g, W1), (W3g, W3), (W2g, W2)):
         assert torch.equal(a, b)
+
+
+def test_a_gemm_that_gives_up_waits_for_its_copies_and_for_nothing_else():
+    """The prefill gate/up GEMM with a stage that never fills: its producer
+    stands before a full ring when the MMA wait runs out.  One wait limit
+    passes, not another one for the stage that never comes."""
+    sh, T, limit = inputs.QWEN3, 2048, 0.2
+    args = _layer(sh, T, 0.35)
+    dsc = abi.desc(T, sh.d, sh.E, sh.I, sh.K, "bf16", sh.renorm)
+    ws = abi.alloc_workspace(dsc, DEV)
+    out, ref = (torch.empty((T, sh.d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    abi.forward(dsc, *args, ref, ws)
+    abi.check(dsc, ws)
+    try:
+        abi.set_fault_injection(abi.FAULT_EXPERT_STAGE, int(limit * 1e9))
+        begin = time.perf_counter()
+        abi.forward(dsc, *args, out, ws)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - begin
+    finally:
+        abi.set_fault_injection(abi.FAULT_NONE, 0)
+    with pytest.raises(abi.BeamError) as ei:
+        abi.check(dsc, ws)
+    assert ei.value.status == 5 and limit <= took < 1.8 * limit, took
+    abi.forward(dsc, *args, out, ws)
+    abi.check(dsc, ws)
+    assert torch.equal(out, ref)

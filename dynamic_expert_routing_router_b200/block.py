@@ -25,16 +25,34 @@ def _empty(*shape, dtype=torch.float32, device=None):
     return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _same_device(what, first, *others):
+    """The kernels take every buffer of a block to be on one device."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise abi.BeamError(1, f"{what}: tensors on {first.device} and {t.device}")
+
+
+def _check_routers(what, W_gate, W_mask, E, d, t):
+    abi._arg(what, "W_gate", W_gate, t, (E, d), None)
+    abi._arg(what, "W_mask", W_mask, t, (E, d), None, True)
+
+
 class Mx4Experts:
-    """The layer's experts with weights and rows in MXFP4, for up to T tokens:
+    """The layer's experts with weights and rows in MXFP4, for T tokens:
     routing and grouping as in the layer, the token rows and the SwiGLU
     activations quantised, both projections as grouped 4-bit products, the
     weighted combine in fp32.
 
-    W1, W3 [E, I, d], W2 [E, d, I] (bf16 or f32) are quantised once; d and I are
-    multiples of 128."""
+    Wg, Wm (or None) [E, d] bf16; W1, W3 [E, I, d], W2 [E, d, I] (bf16 or f32)
+    are quantised once; d and I are multiples of 128."""
 
     def __init__(self, T, d, E, I, K, renorm, Wg, Wm, W1, W3, W2, tau=0.5):
+        _check_routers("Mx4Experts", Wg, Wm, E, d, torch.bfloat16)
+        for name, W, shape in (("W1", W1, (E, I, d)), ("W3", W3, (E, I, d)), ("W2", W2, (E, d, I))):
+            if W.shape != shape:
+                raise abi.BeamError(1, f"Mx4Experts: {name} has to be of shape {shape}, got "
+                                       f"{tuple(W.shape)}")
+        _same_device("Mx4Experts", Wg, Wm, W1, W3, W2)
         self.T, self.d, self.E, self.I, self.K = T, d, E, I, K
         self.Wg, self.Wm = Wg, Wm
         dev = self.device = Wg.device
@@ -68,7 +86,14 @@ class Mx4Experts:
         return codes, scales
 
     def forward(self, x, out, logits=None):
-        """out [T, d] (bf16) for x [T, d] (bf16); logits as abi.route's."""
+        """out [T, d] (bf16) for x [T, d] (bf16); logits f32 [T, 2 E] or None,
+        as abi.route's."""
+        # the calls below take addresses: they see neither shapes nor devices
+        dev, rows = abi._current_device(), (self.T, self.d)
+        abi._arg("Mx4Experts", "x", x, torch.bfloat16, rows, dev)
+        abi._arg("Mx4Experts", "out", out, torch.bfloat16, rows, dev)
+        abi._arg("Mx4Experts", "logits", logits, torch.float32, (self.T, 2 * self.E), dev, True)
+        _same_device("Mx4Experts", self.counts, x)
         if self.T == 0:
             return out
         abi.route(self.dsc, x, self.Wg, self.Wm, self.idx, self.w, self.counts, logits=logits,

@@ -124,19 +124,30 @@ class MoeBlock:
     W_gate, W_mask (or None) [E, d], W1, W3 [E, I, d], W2 [E, d, I]: the layer's;
     w_in [d]; w_out [d], gate_c [d] or None; all of `dtype`.  balance: the
     balance loss's coefficient (training; 0 leaves it out), over n_seq packed
-    sequences; beta weighs the mask-score penalty.  experts: an Mx4Experts that
-    takes the layer's place (serving)."""
+    sequences; beta weighs the mask-score penalty.  experts: an Mx4Experts of
+    the same T, d and E that takes the layer's place (serving, bf16)."""
 
     def __init__(self, T, d, E, I, K, renorm, W_gate, W_mask, W1, W3, W2, w_in, w_out=None,
                  gate_c=None, dtype="bf16", tau=0.5, eps=1e-6, res_scale=1.0, branch_scale=1.0,
                  balance=0.0, n_seq=1, count_kept=False, beta=0.0, train=False, experts=None):
         if train and experts is not None:
             raise ValueError("4-bit experts have no gradients")
+        dev, t = W_gate.device, torch.bfloat16 if dtype == "bf16" else torch.float32
+        if experts is not None:
+            if (experts.T, experts.d, experts.E) != (T, d, E) or t != torch.bfloat16:
+                raise ValueError(f"bf16 experts of T, d, E = {experts.T}, {experts.d}, {experts.E} in a "
+                                 f"{dtype} block of {T}, {d}, {E}")
+            _same_device("MoeBlock", experts.counts, W_gate)
+        else:  # the layer's calls take addresses: they see neither shapes nor devices
+            _check_routers("MoeBlock", W_gate, W_mask, E, d, t)
+            for name, W, shape in (("W1", W1, (E, I, d)), ("W3", W3, (E, I, d)),
+                                   ("W2", W2, (E, d, I))):
+                abi._arg("MoeBlock", name, W, t, shape, None)
+            _same_device("MoeBlock", W_gate, W_mask, W1, W3, W2)
         self.T, self.d, self.E, self.dtype = T, d, E, dtype
         self.layer = (W_gate, W_mask, W1, W3, W2)
         self.w_in, self.w_out, self.gate_c = w_in, w_out, gate_c
         self.experts, self.beta, self.train = experts, beta, train
-        dev, t = W_gate.device, torch.bfloat16 if dtype == "bf16" else torch.float32
         self.dsc = abi.desc(T, d, E, I, K, dtype, renorm, tau=tau)
         self.block = abi.block_desc(T, d, dtype, eps=eps, res_scale=res_scale,
                                     branch_scale=branch_scale, accumulate=True)

@@ -63,3 +63,37 @@ def test_experts_weights(no_launches, name, shape):
     refused("tensors on", block.Mx4Experts, T, D, E, I, K, 1,
             *weights(**{name: weights()[name].to("meta")}).values())
     assert no_launches == []
+
+
+def norms(dtype=BF16):
+    return [torch.ones(D, dtype=dtype)] * 2
+
+
+def test_a_block_takes_experts_of_its_own_size_and_type(no_launches):
+    ex = block.Mx4Experts(T, D, E, I, K, 1, *weights().values())
+    for t, d, e in ((T - 1, D, E), (T + 1, D, E), (T, 2 * D, E), (T, D, 2 * E)):
+        with pytest.raises(ValueError):
+            block.MoeBlock(t, d, e, I, K, 1, *weights().values(), *norms(), experts=ex)
+    with pytest.raises(ValueError):
+        block.MoeBlock(T, D, E, I, K, 1, *weights(torch.float32).values(), *norms(torch.float32), dtype="f32",
+                       experts=ex)
+    refused("tensors on", block.MoeBlock, T, D, E, I, K, 1, torch.zeros(E, D, dtype=BF16, device="meta"), None, None,
+            None, None, *norms(), experts=ex)
+    # the layer's own weights may be gone
+    b = block.MoeBlock(T, D, E, I, K, 1, weights()["Wg"], None, None, None, None, *norms(), experts=ex)
+    assert b.experts is ex and no_launches == []
+
+
+@pytest.mark.parametrize("train", [False, True])
+@pytest.mark.parametrize("name,shape", [("Wg", (E, D - 8)), ("Wm", (E + 8, D)), ("W1", (E, D, I)), ("W3", (E - 1, I, D)),
+                                        ("W2", (E, I, D))])
+def test_a_blocks_weights(no_launches, name, shape, train):
+    f = lambda dtype="bf16", **w: block.MoeBlock(T, D, E, I, K, 1, *weights(**w).values(), *norms(),  # noqa: E731
+                                                 dtype=dtype, train=train, balance=0.1)
+    f()
+    refused("has to be", f, **{name: torch.zeros(shape, dtype=BF16)})
+    refused("has to be", f, **{name: weights(torch.float32)[name]})
+    refused("has to be", f, **{name: weights()[name].transpose(0, 1).contiguous().transpose(0, 1)})
+    refused("tensors on", f, **{name: weights()[name].to("meta")})
+    refused("has to be", f, dtype="f32")
+    assert no_launches == []

@@ -63,7 +63,8 @@ class Mx4Experts:
         u8, i32, bf16 = torch.uint8, torch.int32, torch.bfloat16
         self.up = abi.mx4_desc(N, E, I, d, swiglu=True, out="bf16")
         self.down = abi.mx4_desc(N, E, d, I, out="f32")
-        self.ws = abi.alloc_workspace(self.dsc, dev)
+        # zeroed, as mx4's are: check() may come before a call has written its word
+        self.ws = abi.alloc_workspace(self.dsc, dev).zero_()
         self.ws_up = abi.alloc_mx4_workspace(self.up, dev)
         self.ws_down = abi.alloc_mx4_workspace(self.down, dev)
         self.idx = _empty(T, K, dtype=i32, device=dev)
@@ -153,7 +154,8 @@ class MoeBlock:
                                     branch_scale=branch_scale, accumulate=True)
         self.n = _empty(T, d, dtype=t, device=dev)
         self.y = _empty(T, d, dtype=t, device=dev)
-        self.ws = abi.alloc_workspace(self.dsc, dev) if experts is None else None
+        # zeroed: check() may come before a call has written its error word
+        self.ws = abi.alloc_workspace(self.dsc, dev).zero_() if experts is None else None
         self.loss = torch.zeros(1, device=dev)
         self.bal = None
         if not train:
@@ -165,7 +167,7 @@ class MoeBlock:
                                         count_kept=count_kept, tau=tau, coef=balance)
             i32 = torch.int32
             self.bal_ws = abi.alloc_balance_workspace(self.bal, dev)
-            self.route_ws = abi.alloc_workspace(self.dsc, dev)  # an error word of its own
+            self.route_ws = abi.alloc_workspace(self.dsc, dev).zero_()  # an error word of its own
             self.logits = _empty(T, 2 * E, device=dev)
             self.dlogits = _empty(T, E, device=dev)
             self.cand = _empty(n_seq, E, dtype=i32, device=dev)
@@ -174,7 +176,7 @@ class MoeBlock:
             self.idx = _empty(T, K, dtype=i32, device=dev)
             self.w = _empty(T, K, device=dev)
             self.counts = _empty(E, dtype=i32, device=dev)
-        self.bwd_ws = abi.alloc_backward_workspace(self.dsc, dev)
+        self.bwd_ws = abi.alloc_backward_workspace(self.dsc, dev).zero_()
         self.block_ws = abi.alloc_block_workspace(self.block, dev)
         self.dres = _empty(T, d, dtype=t, device=dev)
         self.dy = _empty(T, d, dtype=t, device=dev)

@@ -97,3 +97,18 @@ def test_a_blocks_weights(no_launches, name, shape, train):
     refused("tensors on", f, **{name: weights()[name].to("meta")})
     refused("has to be", f, dtype="f32")
     assert no_launches == []
+
+
+def test_workspaces_start_without_an_error(no_launches):
+    """check() before the first backward (or forward) reads the words that no
+    call has written yet."""
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)  # fills what torch.empty returns
+    try:
+        assert (torch.empty(64, dtype=torch.uint8) != 0).all()
+        ex = block.Mx4Experts(T, D, E, I, K, 1, *weights().values())
+        b = block.MoeBlock(T, D, E, I, K, 1, *weights().values(), *norms(), train=True, balance=0.1)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    for ws in (ex.ws, ex.ws_up, ex.ws_down, b.ws, b.route_ws, b.bwd_ws):
+        assert (ws == 0).all()

@@ -249,3 +249,18 @@ def test_refusals():
     ex = block.Mx4Experts(3, sh.d, sh.E, sh.I, sh.K, 1, *W)
     with pytest.raises(ValueError):
         block.MoeBlock(3, sh.d, sh.E, sh.I, sh.K, 1, *W, v["w_in"], train=True, experts=ex)
+
+
+def test_check_before_the_first_calls():
+    """In memory that an earlier tensor left full, check() before any call and
+    between the first forward and the first backward reports nothing."""
+    sh = inputs.Shape(128, 8, 2, 128, 1, "bf16")
+    torch.cuda.empty_cache()
+    dirty = [torch.full((1 << k,), 255, dtype=torch.uint8, device=DEV) for k in range(12, 25)]
+    dirty += [torch.full((1 << k,), 255, dtype=torch.uint8, device=DEV) for k in range(12, 25)]
+    torch.cuda.synchronize()
+    del dirty
+    b, v, W = parts(6, sh, "bf16", True, 1, balance=0.1, train=True)
+    b.check()
+    step(b, v, W, back=False)  # checks behind the forward
+    block.Mx4Experts(6, sh.d, sh.E, sh.I, sh.K, 1, *W).check()

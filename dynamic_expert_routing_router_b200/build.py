@@ -4,11 +4,13 @@ the compiled half of the Python binding, from csrc/marshal.cpp.
     python -m dynamic_expert_routing_router_b200.build [--force] [--verbose]
 
 nvcc cross-compiles without a GPU.  The CUDA runtime is linked statically, so
-the library does not depend on which libcudart the host process loaded.
+the library does not depend on which libcudart the host process loaded.  The
+library needs nvcc alone; where torch or g++ is missing it is all that is built.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -57,7 +59,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            *[f"-I{i}" for i in includes], "-o", MARSHAL, src, f"-L{os.path.join(root, 'lib')}",
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
@@ -66,8 +68,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     return MARSHAL
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    build_marshal(force, verbose)
+def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale():
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared",
@@ -76,6 +77,18 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The library, then the binding's compiled half where it can be built."""
+    build_library(force, verbose, extra)
+    for what, there in (("torch", importlib.util.find_spec("torch")), ("g++", shutil.which("g++"))):
+        if not there:
+            print(f"{what} not found: the Python binding's compiled half is not built",
+                  file=sys.stderr)
+            return LIB
+    build_marshal(force, verbose)
     return LIB
 
 

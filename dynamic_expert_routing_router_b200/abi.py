@@ -385,14 +385,21 @@ def _torch():
 
 
 def _marshal():
-    """The compiled half of the binding; raises if it was not built."""
+    """The compiled half of the binding; raises if it was not built, or only for
+    another torch or Python."""
     global _marshal_module
     if _marshal_module is None:
+        from importlib import machinery, util
+
+        from . import build
         _torch()  # its libraries come first
+        path, name = build.marshal_path(), __package__ + "._marshal"
         try:
-            from . import _marshal as m
+            spec = util.spec_from_loader(name, machinery.ExtensionFileLoader(name, path), origin=path)
+            m = util.module_from_spec(spec)
+            spec.loader.exec_module(m)
         except ImportError as e:
-            raise RuntimeError("the module _marshal is missing: build it with "
+            raise RuntimeError(f"the module {os.path.basename(path)} is missing: build it with "
                                "`python -m dynamic_expert_routing_router_b200.build`") from e
         _marshal_module = m
     return _marshal_module

@@ -1,5 +1,5 @@
-"""Build libbeam_moe.so in-tree from csrc/*.cu for sm_100a (B200), and _marshal.so,
-the compiled half of the Python binding, from csrc/marshal.cpp.
+"""Build libbeam_moe.so in-tree from csrc/*.cu for sm_100a (B200), and the compiled
+half of the Python binding, _marshal-<torch and Python>.so, from csrc/marshal.cpp.
 
     python -m dynamic_expert_routing_router_b200.build [--force] [--verbose]
 
@@ -21,7 +21,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbeam_moe.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -46,11 +45,19 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def marshal_path() -> str:
+    """Where the binding's compiled half is for this torch and this Python: it
+    reads torch's C++ objects inline, so one built against another is never
+    loaded, and its name says which it belongs to."""
+    import torch
+    return os.path.join(PKG, f"_marshal-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """g++ against torch's own headers and libraries."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src):
-        return MARSHAL
+    src, path = os.path.join(CSRC, "marshal.cpp"), marshal_path()
+    if not force and os.path.exists(path) and os.path.getmtime(path) >= os.path.getmtime(src):
+        return path
     import sysconfig
 
     import torch
@@ -60,12 +67,15 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
                 sysconfig.get_paths()["include"],
                 os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
-           *[f"-I{i}" for i in includes], "-o", MARSHAL, src, f"-L{os.path.join(root, 'lib')}",
+           *[f"-I{i}" for i in includes], "-o", path, src, f"-L{os.path.join(root, 'lib')}",
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    return MARSHAL
+    for other in glob.glob(os.path.join(PKG, "_marshal*.so")):
+        if other != path:  # of another torch or Python
+            os.remove(other)
+    return path
 
 
 def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:

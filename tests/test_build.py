@@ -1,12 +1,14 @@
 """What the build needs: the library nvcc alone, the binding's compiled half
 torch and g++ too.  No compiler runs here."""
 import importlib.util
+import os
 import shutil
 import subprocess
 
 import pytest
+import torch
 
-from dynamic_expert_routing_router_b200 import build
+from dynamic_expert_routing_router_b200 import abi, build
 
 
 @pytest.fixture
@@ -47,3 +49,20 @@ def test_a_failing_cpp_compiler_comes_after_the_library(commands):
     with pytest.raises(subprocess.CalledProcessError):
         build.build(force=True)
     assert commands[0] == ["nvcc", "g++"]
+
+
+def test_the_binding_belongs_to_one_torch(commands, monkeypatch, tmp_path):
+    """Another torch: the module of the one before is neither kept nor loaded."""
+    assert os.path.exists(build.marshal_path())
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    first = build.marshal_path()
+    for name in (os.path.basename(first), "_marshal.so"):
+        (tmp_path / name).write_bytes(b"")
+        os.utime(tmp_path / name, (2e9, 2e9))  # newer than its source
+    assert build.build_marshal() == first and commands[0] == []
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    monkeypatch.setattr(abi, "_marshal_module", None)
+    with pytest.raises(RuntimeError, match="99.0.*build it"):
+        abi._marshal()
+    assert build.build_marshal() == build.marshal_path() != first and commands[0] == ["g++"]
+    assert os.listdir(tmp_path) == []  # the old ones are gone (and no compiler ran here)

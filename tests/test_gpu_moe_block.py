@@ -264,3 +264,85 @@ def test_check_before_the_first_calls():
     b.check()
     step(b, v, W, back=False)  # checks behind the forward
     block.Mx4Experts(6, sh.d, sh.E, sh.I, sh.K, 1, *W).check()
+
+
+def gradients_in_64_bits(b, v, W, seq, renorm, dl, dout, dn, scales=(1.0, 1.0)):
+    """Autograd of the unmasked block's formula in 64 bits, with the block's own
+    candidates and counts."""
+    leaf = {k: t.double().requires_grad_() for k, t in
+            dict(dx=v["x"], dgt=v["gt"], dwn=v["w_next"], dw_in=b.w_in, dw_out=b.w_out, dgate_c=b.gate_c, dW_gate=W[0],
+                 dW1=W[2], dW3=W[3], dW2=W[4]).items()}
+    x, idx = leaf["dx"], b.idx.long()
+    n = x / rms(x) * leaf["dw_in"]
+    logits = n @ leaf["dW_gate"].T
+    p = torch.softmax(logits, 1)
+    g = torch.softmax(logits.gather(1, idx), 1) if renorm else p.gather(1, idx)
+    y = torch.zeros_like(x)
+    for k in range(idx.shape[1]):
+        e = idx[:, k]
+        h = torch.nn.functional.silu(torch.einsum("td,tid->ti", n, leaf["dW1"][e])) \
+            * torch.einsum("td,tid->ti", n, leaf["dW3"][e])
+        y = y + g[:, k:k + 1] * torch.einsum("ti,tdi->td", h, leaf["dW2"][e])
+    branch = torch.sigmoid(leaf["dgt"])[:, None] * leaf["dgate_c"] * leaf["dw_out"] * y / rms(y)
+    out = scales[0] * x + scales[1] * branch
+    n_next = out / rms(out) * leaf["dwn"]
+    loss, S, E = 0.0, len(seq) - 1, W[0].shape[0]
+    for s, (lo, hi) in enumerate(zip(seq[:-1], seq[1:])):
+        f = b.cand[s].double() * E / (idx.shape[1] * (hi - lo))
+        loss = loss + b.bal.coef / S * (f * p[lo:hi].mean(0)).sum()
+    ((dout.double() * out).sum() + (dn.double() * n_next).sum() + dl * loss).backward()
+    return {k: t.grad for k, t in leaf.items()}
+
+
+@pytest.mark.parametrize("upstream", [1.0, 0.0], ids=["all", "balance_alone"])
+@pytest.mark.parametrize("T,sh", [(12, inputs.Shape(128, 8, 2, 128, 1, "f32")), (40, inputs.Shape(256, 16, 4, 128, 0, "f32"))],
+                         ids=["T12", "T40_all_softmax"])
+def test_gradients_are_those_of_the_formula_in_64_bits(T, sh, upstream):
+    """An fp32 block without a mask against autograd in 64 bits, with the
+    rows' upstream gradients and with the balance loss's alone, which then hides
+    behind nothing.
+
+    Bar, normwise: forward values are off by at most (d + I + 500) u of their
+    magnitudes' sum, each gradient by the same once more on its way back, and
+    magnitudes add up to at most sqrt(d) = 16 times what the signed sums of
+    random terms come to: 2 x 884 x 16 u = 1.7e-3 of the largest entry.  A part
+    that is missing changes it by a share of one."""
+    seq = [0, 5, T]
+    b, v, W = parts(T, sh, "f32", False, 3, balance=0.5, n_seq=2, train=True, res_scale=0.9, branch_scale=0.5)
+    for k in ("dout", "dn"):
+        v[k] *= upstream
+    got = step(b, v, W, torch.tensor([2.0], device=DEV), torch.tensor(seq, dtype=torch.int32, device=DEV))
+    want = gradients_in_64_bits(b, v, W, seq, sh.renorm, 2.0, v["dout"], v["dn"], (0.9, 0.5))
+    for k, w in want.items():
+        if w is None or not w.abs().max() > 0:
+            assert upstream == 0.0 and k not in ("dx", "dw_in", "dW_gate") and (got[k] == 0).all(), k
+            continue
+        assert float((got[k].double() - w).abs().max()) <= 1.7e-3 * float(w.abs().max()), k
+
+
+def test_two_blocks_train_on_two_streams_at_once():
+    """Blocks share no buffer: steps of two of them that overlap give what they
+    give one after the other."""
+    sh, T = inputs.Shape(256, 16, 4, 256, 1, "bf16"), 200
+    seq = torch.tensor([0, 90, T], dtype=torch.int32, device=DEV)
+    dl = torch.tensor([0.7], device=DEV)
+    made = [parts(T, sh, "bf16", True, s, balance=0.1, n_seq=2, beta=0.01, train=True) for s in (11, 12)]
+    want = [step(*m, dl, seq) for m in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    own = [dict(out=torch.empty_like(v["x"]), n=torch.empty_like(v["x"]), dx=torch.empty_like(v["x"]),
+                dgt=torch.empty(T, device=DEV), dwn=torch.zeros(sh.d, device=DEV)) for _, v, _ in made]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (b, v, _), o, s in zip(made, own, streams):
+            with torch.cuda.stream(s):
+                b.zero_grad()
+                o["dwn"].zero_()
+                b.forward(v["x"], o["out"], gate_t=v["gt"], w_next=v["w_next"], n_next=o["n"], seq_begin=seq)
+                b.backward(v["x"], o["out"], v["dout"], o["dx"], gate_t=v["gt"], dgate_t=o["dgt"], w_next=v["w_next"],
+                           dn_next=v["dn"], dw_next=o["dwn"], seq_begin=seq, dloss=dl)
+    torch.cuda.synchronize()
+    for (b, _, _), o, w in zip(made, own, want):
+        b.check()
+        for k, t in dict(out=o["out"], n_next=o["n"], loss=b.loss, dx=o["dx"], dgt=o["dgt"], dwn=o["dwn"],
+                         **{"d" + k: g for k, g in b.grads.items()}).items():
+            assert torch.equal(t, w[k]), k

@@ -318,3 +318,20 @@ def test_offsets_past_32_bits_and_many_sequences():
     rl, _, _, g = reference(lg, E, 2, list(range(0, T + 1, 3)), 1.0, c)
     assert abs(float(loss) - float(rl)) <= (80 + S) * U * float(rl)
     assert ((dl.double() - g).abs() <= 150 * U * E).all()
+
+
+def test_many_sequences_entry_by_entry():
+    """3000 sequences of three tokens, where a gradient's entry is of the order
+    of 1e-5: each within 150 u of its own terms' magnitudes."""
+    T, E, K, S = 9000, 20, 2, 3000
+    lg, begin = logits_of(T, E, 1, False), list(range(0, 9001, 3))
+    b = torch.tensor(begin, dtype=torch.int32, device=DEV)
+    dsc = abi.balance_desc(T, E, K, n_seq=S)
+    cand, dl = torch.empty(S, E, dtype=torch.int32, device=DEV), torch.full((T, E), float("nan"), device=DEV)
+    abi.balance(dsc, lg, torch.empty(1, device=DEV), cand, abi.alloc_balance_workspace(dsc), seq_begin=b)
+    abi.balance_backward(dsc, lg, cand, dl, seq_begin=b)
+    p = torch.softmax(lg.double(), 1)
+    f = counts_of(lg, E, K)[0].view(S, 3, E).sum(1).repeat_interleave(3, 0) * E / (K * 3)
+    dot = (p * f).sum(1, keepdim=True)
+    g, mag = p * (f - dot) / (3 * S), p * (f + dot) / (3 * S)
+    assert ((dl.double() - g).abs() <= 150 * U * mag + 1e-38).all()

@@ -363,3 +363,15 @@ def test_a_call_that_gives_up_waits_for_its_copies_and_for_nothing_else(k):
     abi.mx4_expert_product(dsc, *a, c, ws[0][0], tiled, y, wk)
     abi.mx4_check(dsc, wk)
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("swiglu", [False, True], ids=["plain", "swiglu"])
+@pytest.mark.parametrize("counts", [[40, 0, 64, 23, 1], [100, 0, 3, 65, 20], [64] * 30])
+def test_tiles_of_64_rows_match_fp64(counts, swiglu, out):
+    """17 to 64 rows of capacity per expert: full, unfilled and several tiles."""
+    n, k = 256, 640
+    a, ws = operands(counts, n, k, sum(counts), swiglu=swiglu, tail=3)
+    y, dsc, wk = product(counts, n, k, a, ws, out)
+    abi.mx4_check(dsc, wk)
+    assert_product(y, counts, n, k, a, ws, out)

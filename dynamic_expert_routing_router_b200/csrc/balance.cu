@@ -29,8 +29,12 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBalWarps = 8;
-// Batches that one cluster takes: eight CTAs of 32 tokens, a barrier a sequence.
-constexpr int kSmallTokens = 256, kSmallSeqs = 4;
+// One sequence of so many tokens goes to one cluster, up to eight CTAs of 32
+// tokens.  A pass with K = 8 there against the two launches: 64 x 128 4.5 / 6.5
+// us, 256 x 256 7.4 / 7.5.  Several sequences would take their turns there, a
+// cluster barrier each: two of 64 x 128 7.6 / 6.4 us, of 256 x 128 11.2 / 6.3,
+// four 13.0 / 6.5 and 20.3 / 6.6.
+constexpr int kSmallTokens = 256;
 constexpr int kMaxChunk = 1 << 18;  // tokens: a warp's counts fit 16 bits
 
 // Sequence boundaries as given, made safe: inside [0, T] and not decreasing.
@@ -286,11 +290,10 @@ __device__ __forceinline__ float finish_expert(const BalanceArgs &a, int s, int 
     return float(a.count_kept ? k : c) * float(a.E) / (float(a.K) * len) * (p / len);
 }
 
-// A small batch in one launch: one cluster, CTA r takes the tokens [r C, (r +
-// 1) C), and of each sequence in turn adds up the experts r, r + CTAs, ... of
-// all CTAs through their shared memory (two buffers in turn, so that one
-// cluster barrier per sequence does).  128 tokens of 128 experts take 5.4 us;
-// two launches took 6.6, and the host 2.5 more.
+// A small batch of one sequence in one launch: one cluster, CTA r takes the
+// tokens [r C, (r + 1) C), and adds up the experts r, r + CTAs, ... of all CTAs
+// through their shared memory.  128 tokens of 128 experts take 4.5 to 5.1 us on
+// the GPU, by how the logits lie, and 5.0 to 5.4 a pass; two launches 6.0 and 6.5.
 template <int EPL>
 __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const BalanceArgs a) {
     namespace cg = cooperative_groups;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
         float p[32 * EPL];
         int c[32 * EPL], k[32 * EPL];
     };
-    __shared__ Part part[2];
+    __shared__ Part mine;
     __shared__ float s_terms[8];  // of rank 0: the CTAs' terms
     cg::cluster_group cluster = cg::this_cluster();
     griddep_wait();
@@ -308,38 +311,33 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
     const int ctas = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int t0 = rank * a.C, t1 = min(a.T, t0 + a.C);
     const bool mask = a.has_mask && (a.kept || a.count_kept);
+    const Span sp = span_of(a, 0);
+    float acc[EPL];
+    unsigned count[EPL];
+    float r[EPL];
+    add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), r, false, acc, count);
+    sums.put(acc, count);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        float v = 0.0f;
+        int c = 0, k = 0;
+        sums.add(e, &v, &c, &k);
+        mine.p[e] = v;
+        mine.c[e] = c;
+        mine.k[e] = k;
+    }
+    cluster.sync();
     float term = 0.0f;  // of this thread's experts
-    bool bad = false;
-    for (int s = 0; s < a.S; ++s) {
-        const Span sp = span_of(a, s);
-        bad |= sp.bad;
-        float acc[EPL];
-        unsigned count[EPL];
-        float r[EPL];
-        add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), r, false, acc, count);
-        sums.put(acc, count);
-        __syncthreads();
-        Part &mine = part[s & 1];
-        for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-            float v = 0.0f;
-            int c = 0, k = 0;
-            sums.add(e, &v, &c, &k);
-            mine.p[e] = v;
-            mine.c[e] = c;
-            mine.k[e] = k;
+    for (int e = rank + int(threadIdx.x) * ctas; e < a.E; e += blockDim.x * ctas) {
+        float v = 0.0f;
+        int c = 0, k = 0;
+        for (int q = 0; q < ctas; ++q) {
+            const Part *from = cluster.map_shared_rank(&mine, q);
+            v += from->p[e];
+            c += from->c[e];
+            k += from->k[e];
         }
-        cluster.sync();
-        for (int e = rank + int(threadIdx.x) * ctas; e < a.E; e += blockDim.x * ctas) {
-            float v = 0.0f;
-            int c = 0, k = 0;
-            for (int r = 0; r < ctas; ++r) {
-                const Part *from = cluster.map_shared_rank(&mine, r);
-                v += from->p[e];
-                c += from->c[e];
-                k += from->k[e];
-            }
-            term += finish_expert(a, s, e, sp, v, c, k);
-        }
+        term += finish_expert(a, 0, e, sp, v, c, k);
     }
     // the CTAs' terms, in order
     term = warp_sum(term);
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
     if (rank == 0 && threadIdx.x == 0) {
         float v = 0.0f;
         for (int r = 0; r < ctas; ++r) v += s_terms[r];
-        *a.loss = bad ? NAN : a.coef / float(a.S) * v;
+        *a.loss = sp.bad ? NAN : a.coef * v;
     }
 }
 
@@ -623,7 +621,7 @@ beam_status beam_moe_balance(const beam_balance_desc *desc, const float *logits,
     a.kept = kept_counts;
     a.prob = mean_prob;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (desc->T <= kSmallTokens && desc->n_seq <= kSmallSeqs) {
+    if (desc->T <= kSmallTokens && desc->n_seq == 1) {
         const int ctas = desc->T <= 16 ? 1 : desc->T <= 32 ? 2 : desc->T <= 64 ? 4 : 8;
         a.C = (desc->T + ctas - 1) / ctas;
         return by_experts<Small>(desc->E, a, ctas, st) == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA;

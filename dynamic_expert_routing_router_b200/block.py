@@ -126,7 +126,11 @@ class MoeBlock:
     w_in [d]; w_out [d], gate_c [d] or None; all of `dtype`.  balance: the
     balance loss's coefficient (training; 0 leaves it out), over n_seq packed
     sequences; beta weighs the mask-score penalty.  experts: an Mx4Experts of
-    the same T, d and E that takes the layer's place (serving, bf16)."""
+    the same T, d and E that takes the layer's place (serving, bf16).
+
+    No shared experts: a block that has them calls abi.forward_shared between
+    abi.block_enter and abi.block_exit itself, and gate_t gates all of y, not
+    a shared branch alone."""
 
     def __init__(self, T, d, E, I, K, renorm, W_gate, W_mask, W1, W3, W2, w_in, w_out=None,
                  gate_c=None, dtype="bf16", tau=0.5, eps=1e-6, res_scale=1.0, branch_scale=1.0,

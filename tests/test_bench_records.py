@@ -57,3 +57,10 @@ def test_other_workload_or_kernel_gives_no_traffic(tmp_path, monkeypatch):
     assert bench.recorded_traffic("experts_fused_gate_up_down", 128, 0.35)[0] is None
     assert bench.recorded_traffic("router_gemm", 128, 0.15)[0] is None
     assert bench.recorded_traffic("experts_fused_gate_up_down", 128, 0.15)[0] is not None
+
+
+def test_the_committed_record_is_of_the_sources_as_they_are():
+    """A change of the kernel's sources takes the figure out of the benchmark's
+    line until the record is taken again."""
+    traffic, source = bench.recorded_traffic("experts_fused_gate_up_down", 128, 0.15)
+    assert traffic and source == bench.TRAFFIC_RECORDS[0], source

@@ -346,3 +346,29 @@ def test_two_blocks_train_on_two_streams_at_once():
         for k, t in dict(out=o["out"], n_next=o["n"], loss=b.loss, dx=o["dx"], dgt=o["dgt"], dwn=o["dwn"],
                          **{"d" + k: g for k, g in b.grads.items()}).items():
             assert torch.equal(t, w[k]), k
+
+
+def test_no_tokens_and_rows_of_another_number():
+    """A block of no tokens runs and leaves the gradients as they were; rows of
+    another number than the block's or the experts' are refused."""
+    sh = inputs.Shape(128, 8, 2, 128, 1, "bf16")
+    b, v, W = parts(0, sh, "bf16", True, 1, balance=0.1, n_seq=2, train=True)
+    seq = torch.zeros(3, dtype=torch.int32, device=DEV)
+    out, n, dx = (torch.empty_like(v["x"]) for _ in range(3))
+    for g in b.grads.values():
+        g.fill_(3.0)
+    b.forward(v["x"], out, w_next=v["w_next"], n_next=n, seq_begin=seq)
+    dwn = torch.full((sh.d,), 3.0, device=DEV)
+    b.backward(v["x"], out, v["dout"], dx, w_next=v["w_next"], dn_next=v["dn"], dw_next=dwn, seq_begin=seq)
+    b.check()
+    assert float(b.loss) == 0.0 and all((g == 3.0).all() for g in (dwn, *b.grads.values()))
+    ex = block.Mx4Experts(6, sh.d, sh.E, sh.I, sh.K, 1, *W)
+    rows = torch.zeros(7, sh.d, dtype=BF16, device=DEV)
+    for x, y in ((rows[:5], rows[:5]), (rows[:6], rows[:5]), (rows, rows[:6])):
+        with pytest.raises(abi.BeamError):
+            ex.forward(x, y)
+    served = block.MoeBlock(6, sh.d, sh.E, sh.I, sh.K, 1, *W, v["w_in"], experts=ex)
+    for x, y in ((rows[:5], rows[:5]), (rows[:6], rows)):
+        with pytest.raises(abi.BeamError):
+            served.forward(x, y)
+    assert ex.forward(rows[:6], torch.empty_like(rows[:6])).isfinite().all()

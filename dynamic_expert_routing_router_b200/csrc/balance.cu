@@ -22,8 +22,8 @@
 // Bound by instructions: about 515 a token of 256 experts, half of them for the
 // 8 largest, against 1 KB of logits and a 32-byte sector of mask logits for each
 // candidate.  32768 such tokens with a mask take 28.5 us (1.5 TB/s), the second
-// launch 5 of them; the gradient of 17937 x 239 10.3 us (3.3 TB/s): four
-// reductions a token that wait for one another, one token of a warp at a time.
+// launch 5 of them; the gradient of 17937 x 239, about 400 instructions a token,
+// 10.3 us (3.3 TB/s).
 #include <cooperative_groups.h>
 
 #include "beam_internal.h"

@@ -316,11 +316,13 @@ __global__ void __launch_bounds__(kBalWarps * 32) balance_small_kernel(const Bal
     const int ctas = int(cluster.num_blocks()), rank = int(cluster.block_rank());
     const int t0 = rank * a.C, t1 = min(a.T, t0 + a.C);
     const bool mask = a.has_mask && (a.kept || a.count_kept);
+    float r[EPL];  // the first token's logits come while the boundaries do
+    if (t0 + warp < t1) load_row(a.logits + (long long)(t0 + warp) * a.ld, a.E, r);
     const Span sp = span_of(a, 0);
+    const int lo = max(sp.lo, t0);
     float acc[EPL];
     unsigned count[EPL];
-    float r[EPL];
-    add_tokens(a, mask, max(sp.lo, t0) + warp, min(sp.hi, t1), r, false, acc, count);
+    add_tokens(a, mask, lo + warp, min(sp.hi, t1), r, lo == t0, acc, count);
     sums.put(acc, count);
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
